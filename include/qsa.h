@@ -449,6 +449,183 @@ qsa_status qsa_sparse_prefill(const qsa_cache *cache, int32_t B, int32_t n_token
                               size_t workspace_bytes, qsa_stream_t stream);
 
 /*
+ * Attention over whole key ranges of the paged K/V cache, and the call that
+ * writes that cache.  The pages leave these to the serving runtime around the
+ * path; they work on the same qsa_cache (its kc and ring are not used and may
+ * be NULL / empty here), with the same head shapes and types:
+ *   - head_dim 64 or 128, Hq % Hkv == 0;
+ *   - F32 caches take F32 queries, BF16 and FP8 caches BF16 queries; o has the
+ *     type of q, lse is float32 (natural log);
+ *   - FP8 values are code * scale[page][kv head];
+ *   - sums, softmax statistics and partial results are float32; for BF16 and
+ *     FP8 caches the softmax weights enter the value product rounded to 16
+ *     bits (relative 2^-9 or less, the error of o's own rounding).
+ * A query that sees no key gives o = 0 and lse = -inf; a request of length 0
+ * (a padding row of a batch) is one.  Keys that no query of a call sees are
+ * never read, and their pages may be unmapped (-1).  K and V rows that some
+ * query of the call sees have to be finite where another query of the same
+ * request does not see them.
+ * Lengths, offsets and tables live on the device; the host bounds (max_...)
+ * size the launch.  Recorded on the device: QSA_ERR_BOUNDS for a length that
+ * the block table cannot hold (cut to what it can) and for a missing page (its
+ * keys and values read as zeros); QSA_ERR_BAD_INPUT for malformed offsets
+ * (their rows are left out).
+ * Workspaces: 256-byte aligned, any contents, nothing is kept between calls;
+ * calls that overlap on the GPU (captured graphs too) need separate ones.  Where
+ * a *_workspace_bytes call returns 0 the workspace may be NULL.
+ * All calls can be captured into a graph.
+ */
+
+typedef enum { QSA_ROPE_HALF = 0, QSA_ROPE_INTERLEAVED = 1 } qsa_rope_layout;
+typedef enum {
+  QSA_ROPE_SCALING_NONE = 0,
+  QSA_ROPE_SCALING_LINEAR = 1, /* every frequency divided by factor             */
+  QSA_ROPE_SCALING_NTK = 2,    /* theta * factor^(R / (R - 2))                  */
+  QSA_ROPE_SCALING_YARN = 3    /* by turns over the trained length, with mscale */
+} qsa_rope_scaling;
+
+/*
+ * qsa_rope_freqs — the frequencies of qsa_rope_append (host only, no GPU work).
+ *
+ *   rotary_dim R  even, 0 .. 128; pair i of R / 2 turns by
+ *       f_i = theta^(-2 i / R) radians per token        (theta > 1)
+ *   LINEAR  f_i / factor
+ *   NTK     theta replaced by theta * factor^(R / (R - 2))  (R > 2)
+ *   YARN    a pair that turns at least beta_fast times over
+ *           original_max_position tokens keeps f_i, one that turns at most
+ *           beta_slow times gets f_i / factor, in between linear in i:
+ *           d(beta) = R ln(original_max_position / (2 pi beta)) / (2 ln theta),
+ *           low = max(floor d(beta_fast), 0), high = min(ceil d(beta_slow), R - 1),
+ *           r_i = clamp((i - low) / max(high - low, 0.001), 0, 1),
+ *           f_i (1 - r_i) + f_i / factor r_i;  mscale = 0.1 ln(factor) + 1
+ *   factor >= 1
+ *   inv_freq [R/2] double: the f_i, or NULL
+ *   freqs    [R/2]: f_i / (2 pi) turns per token in units of 2^-64 (modulo a
+ *            turn), what qsa_rope_append takes (copied to the device)
+ *   mscale   factor on the rotated dims (1 except for YARN)
+ * Errors: QSA_ERR_INVALID_ARG.
+ */
+qsa_status qsa_rope_freqs(int32_t rotary_dim, double theta, int32_t scaling, double factor,
+                          int32_t original_max_position, double beta_fast, double beta_slow,
+                          double *inv_freq, uint64_t *freqs, float *mscale);
+
+/*
+ * qsa_rope_append — rotary positions on new queries and keys, and the append
+ * of the new K/V rows to the paged cache.
+ *
+ * Passage: PR #53896 report, file list (apply_qsa_rope, 1D positions); the
+ * append is the write that qsa_sparse_decode and the calls below read.
+ * Token j of request r sits at position p = pos0[r] + j.  The first R dims of
+ * each query and key head are pairs (a, b): (i, i + R/2) with QSA_ROPE_HALF,
+ * (2i, 2i + 1) with QSA_ROPE_INTERLEAVED; pair i becomes
+ *   mscale * (x_a cos(p f_i) - x_b sin(p f_i)),
+ *   mscale * (x_a sin(p f_i) + x_b cos(p f_i)).
+ * The dims behind R and the values pass unchanged.  q_out gets the queries;
+ * the key and value rows go to position p's place in the cache.
+ *
+ *   pos0 [B], cu_new [B+1]  int32 as qsa_compress_append (cu_new[0] = 0)
+ *   n_tokens  rows of q, k, v and q_out; rows from cu_new[B] on (padding of a
+ *             batch of fixed size) are neither read into the cache nor written
+ *   q [n_tokens, Hq, D], k, v [n_tokens, Hkv, D] of dtype; row strides
+ *             q_stride, k_stride, v_stride in elements (heads are dense, so
+ *             the parts of a fused projection's rows pass without a copy)
+ *   dtype     QSA_F32 for F32 caches, QSA_BF16 for BF16 and FP8 caches
+ *   freqs     [R/2] uint64 on the device (qsa_rope_freqs)
+ *   layout    qsa_rope_layout;  R = rotary_dim even, 0 .. D
+ *   q_out     [n_tokens, Hq, D] of dtype, dense; may be q itself when q is dense
+ * Angles are exact to 2^-24 half turns at every position.  BF16 and FP8 rows
+ * are rounded to nearest even once; FP8 codes are value / scale[page][kv head]
+ * (scales set by the caller beforehand, > 0), saturated at 448.
+ * Two tokens of one call must not share a position of the cache.
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (types, head_dim); on the
+ * device QSA_ERR_BOUNDS for a position without a page (its query is still
+ * rotated).
+ */
+qsa_status qsa_rope_append(const qsa_cache *cache, int32_t B, int32_t n_tokens, const int32_t *pos0,
+                           const int32_t *cu_new, const void *q, int64_t q_stride, const void *k,
+                           int64_t k_stride, const void *v, int64_t v_stride, int32_t dtype,
+                           int32_t Hq, const uint64_t *freqs, int32_t rotary_dim, int32_t layout,
+                           float mscale, void *q_out, qsa_stream_t stream);
+
+/*
+ * qsa_window_decode — decode attention over a sliding window and the first
+ * tokens (sinks) of each request.
+ *
+ * Query token t of request r sits at p = ctx_lens[r] - T + t and sees the
+ * keys i <= p with i > p - window or i < sinks (its own key is one of the
+ * window's `window` keys).  window = INT32_MAX is dense causal attention.
+ *
+ *   q    [B, T, Hq, D], T 1 .. 4, (Hq / Hkv) * T <= 32, 16-byte aligned
+ *   ctx_lens [B] int32 cached tokens (>= T; shorter: the query tokens before
+ *            position 0 see nothing)
+ *   window >= 1, sinks >= 0
+ *   o    [B, T, Hq, D] of q_dtype, 16-byte aligned;  lse [B, T, Hq] float32
+ *   workspace >= qsa_window_decode_workspace_bytes(...) (the cache's geometry
+ *            is read, not its pointers)
+ * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (types, head shapes, B
+ * above 65535).
+ */
+size_t qsa_window_decode_workspace_bytes(const qsa_cache *cache, int32_t B, int32_t T, int32_t Hq,
+                                         int32_t window, int32_t sinks);
+qsa_status qsa_window_decode(const qsa_cache *cache, int32_t B, int32_t T, int32_t Hq, const void *q,
+                             int32_t q_dtype, const int32_t *ctx_lens, int32_t window, int32_t sinks,
+                             float sm_scale, void *o, float *lse, void *workspace,
+                             size_t workspace_bytes, qsa_stream_t stream);
+
+/*
+ * qsa_window_prefill — the same visibility for a prefill chunk: the newest
+ * n_r = cu_q[r+1] - cu_q[r] tokens of each request are its query tokens (their
+ * K/V rows are in the cache), token j at position ctx_lens[r] - n_r + j.
+ *
+ *   cu_q [B+1] int32 (cu_q[0] = 0);  rows from cu_q[B] on are left as they were
+ *   n_tokens       rows of q, o and lse
+ *   max_q_per_req  host bound of n_r; a longer request is left out
+ *                  (QSA_ERR_BAD_INPUT on the device)
+ *   q [n_tokens, Hq, D], o alike, lse [n_tokens, Hq]; Hq / Hkv <= 32
+ *   the others as qsa_window_decode
+ */
+size_t qsa_window_prefill_workspace_bytes(const qsa_cache *cache, int32_t B, int32_t n_tokens,
+                                          int32_t max_q_per_req, int32_t Hq, int32_t window,
+                                          int32_t sinks);
+qsa_status qsa_window_prefill(const qsa_cache *cache, int32_t B, int32_t n_tokens,
+                              int32_t max_q_per_req, const int32_t *cu_q, const int32_t *ctx_lens,
+                              const void *q, int32_t q_dtype, int32_t Hq, int32_t window,
+                              int32_t sinks, float sm_scale, void *o, float *lse, void *workspace,
+                              size_t workspace_bytes, qsa_stream_t stream);
+
+/*
+ * qsa_prefix_decode — exact decode attention of a batch whose requests share
+ * long prefixes: each prefix's K/V are read once for its whole group.
+ *
+ * Requests cu_group[g] .. cu_group[g+1]-1 form group g; their first
+ * prefix_lens[g] keys are the same, and are read through the block-table row
+ * of the group's first request.  Keys from prefix_lens[g] on are each
+ * request's own.  Query token t of request r sees every key i <=
+ * ctx_lens[r] - T + t (a prefix longer than that is cut for it).  The prefix
+ * and the tail are two partial results merged by log-sum-exp, as the KV
+ * partitions of qsa_sparse_decode are.
+ *
+ *   cu_group [n_groups+1], prefix_lens [n_groups] int32; a request in no
+ *            group (before cu_group[0], from cu_group[n_groups] on) shares
+ *            nothing; a group may be empty, a prefix 0
+ *   max_group   host bound of a group's requests, 1 .. B; a larger group is
+ *               recorded as QSA_ERR_BAD_INPUT and its prefix left out
+ *   max_prefix, max_tail  expected bounds of prefix_lens and of
+ *               ctx_lens - prefix_lens (they only choose how the work is
+ *               split: longer ones are right, and slower)
+ *   the others as qsa_window_decode
+ */
+size_t qsa_prefix_decode_workspace_bytes(const qsa_cache *cache, int32_t B, int32_t T, int32_t Hq,
+                                         int32_t n_groups, int32_t max_group, int32_t max_prefix,
+                                         int32_t max_tail);
+qsa_status qsa_prefix_decode(const qsa_cache *cache, int32_t B, int32_t T, int32_t Hq, const void *q,
+                             int32_t q_dtype, const int32_t *ctx_lens, int32_t n_groups,
+                             const int32_t *cu_group, const int32_t *prefix_lens, int32_t max_group,
+                             int32_t max_prefix, int32_t max_tail, float sm_scale, void *o,
+                             float *lse, void *workspace, size_t workspace_bytes,
+                             qsa_stream_t stream);
+
+/*
  * qsa_index_topk_noalloc — qsa_index_topk without a caller workspace.
  *
  * The source pages have no counterpart to this entry point; it exists for

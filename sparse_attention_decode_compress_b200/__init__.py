@@ -7,6 +7,10 @@ from .api import (QSACache, QSAError, QSASession, allocate_norm_caches, new_work
                   qsa_index_topk_tokens, qsa_index_topk_workspace_bytes, qsa_lse_merge,
                   qsa_sparse_decode, qsa_sparse_decode_merged, qsa_sparse_decode_splits,
                   qsa_sparse_decode_workspace_bytes)
+from .attention import (QSAPrefixDecode, QSARopeAppend, QSAWindowDecode, QSAWindowPrefill,
+                        qsa_prefix_decode, qsa_prefix_decode_workspace_bytes, qsa_rope_append,
+                        qsa_rope_freqs, qsa_window_decode, qsa_window_decode_workspace_bytes,
+                        qsa_window_prefill, qsa_window_prefill_workspace_bytes)
 from .dcp import DCPDecode, dcp_exchange
 from .decode import QSADecodeStep, QSADraftDecode
 
@@ -19,4 +23,7 @@ __all__ = [
     "qsa_index_topk_workspace_bytes", "qsa_lse_merge",
     "qsa_sparse_decode", "qsa_sparse_decode_merged", "qsa_sparse_decode_splits",
     "qsa_sparse_decode_workspace_bytes",
+    "QSAPrefixDecode", "QSARopeAppend", "QSAWindowDecode", "QSAWindowPrefill", "qsa_prefix_decode",
+    "qsa_prefix_decode_workspace_bytes", "qsa_rope_append", "qsa_rope_freqs", "qsa_window_decode",
+    "qsa_window_decode_workspace_bytes", "qsa_window_prefill", "qsa_window_prefill_workspace_bytes",
 ]

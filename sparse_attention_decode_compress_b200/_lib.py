@@ -8,6 +8,7 @@ from .build import LIB_PATH
 
 c_int32, c_int64, c_size_t, c_void_p, c_float = (ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                                                  ctypes.c_void_p, ctypes.c_float)
+c_double = ctypes.c_double
 
 QSA_OK = 0
 QSA_F32, QSA_BF16, QSA_FP8_E4M3 = 0, 1, 2
@@ -67,6 +68,26 @@ SIGNATURES = {
                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
                                      c_int32, c_int32, c_int32, c_float, c_void_p, c_void_p,
                                      c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qsa_rope_freqs": (c_int32, [c_int32, c_double, c_int32, c_double, c_int32, c_double, c_double,
+                                 c_void_p, c_void_p, ctypes.POINTER(c_float)]),
+    "qsa_rope_append": (c_int32, [ctypes.POINTER(QsaCacheStruct), c_int32, c_int32, c_void_p,
+                                  c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                  c_int32, c_int32, c_void_p, c_int32, c_int32, c_float, c_void_p,
+                                  c_void_p]),
+    "qsa_window_decode_workspace_bytes": (c_size_t, [ctypes.POINTER(QsaCacheStruct)] + [c_int32] * 5),
+    "qsa_window_decode": (c_int32, [ctypes.POINTER(QsaCacheStruct), c_int32, c_int32, c_int32,
+                                    c_void_p, c_int32, c_void_p, c_int32, c_int32, c_float, c_void_p,
+                                    c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qsa_window_prefill_workspace_bytes": (c_size_t, [ctypes.POINTER(QsaCacheStruct)] + [c_int32] * 6),
+    "qsa_window_prefill": (c_int32, [ctypes.POINTER(QsaCacheStruct), c_int32, c_int32, c_int32,
+                                     c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                                     c_int32, c_float, c_void_p, c_void_p, c_void_p, c_size_t,
+                                     c_void_p]),
+    "qsa_prefix_decode_workspace_bytes": (c_size_t, [ctypes.POINTER(QsaCacheStruct)] + [c_int32] * 7),
+    "qsa_prefix_decode": (c_int32, [ctypes.POINTER(QsaCacheStruct), c_int32, c_int32, c_int32,
+                                    c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+                                    c_int32, c_int32, c_int32, c_float, c_void_p, c_void_p, c_void_p,
+                                    c_size_t, c_void_p]),
     "qsa_get_device_error": (c_int32, [c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
     "qsa_session_create": (c_int32, [ctypes.POINTER(QsaCacheStruct), c_int32, c_int32, c_int32,
                                      c_int32, c_int32, c_int32, c_int32, c_int32, c_float,

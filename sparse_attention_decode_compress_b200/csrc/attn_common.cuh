@@ -1,0 +1,261 @@
+// What the attention calls over whole key ranges share (qsa_window_decode,
+// qsa_window_prefill, qsa_prefix_decode): which keys a query sees, how query
+// rows and keys are numbered, and the merge of partial results.
+//
+// A call attends SEQUENCES of consecutive query tokens, all of whose keys are
+// read through one block-table row:
+//   kWindow, cu == NULL   request s: its T newest tokens (decode)
+//   kWindow, cu != NULL   request s: tokens cu[s] .. cu[s+1]-1, its newest (chunk)
+//   kShared               group s of requests cu[s] .. cu[s+1]-1, T tokens
+//                         each, over the first prefix_lens[s] keys that all of
+//                         them share (read through the first request's row)
+//   kTail                 request s: its T newest tokens over the keys behind
+//                         its group's prefix
+// A query at position p sees the keys i of
+//   kWindow   i <= p and (i > p - window or i < sinks)
+//   kShared   i <= p and i < prefix
+//   kTail     i <= p and i >= prefix
+// so always i < hi and (i >= lo or i < sink) with per-token hi, lo.
+//
+// The query heads of one kv head are rows of one small matrix: row
+// m = token * G + head-in-group of a sequence (G = Hq / Hkv), cut into tiles.
+// The keys a tile needs are one or two ranges, [0, sa) and [b0, b1); they are
+// walked as one VIRTUAL range [0, sa + b1 - b0).  sa and b0 are multiples of 4,
+// the page sizes too, so four virtual keys from a multiple of 4 on always lie
+// in one page.
+#pragma once
+#include "qsa_common.cuh"
+
+namespace qsa {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxT = 4;      // query tokens per request of the decode calls
+constexpr int kMaxGroup = 32;  // query heads per kv head (times T in the decode calls)
+
+enum Mode { kWindow = 0, kShared = 1, kTail = 2 };
+
+struct Args {
+  CacheDev c;
+  const void *q;  // [n_tok, Hq, D]
+  void *o;        // [n_tok, Hq, D] of the query type
+  float *lse;     // [n_tok, Hq]
+  int B, T, Hq, G, n_tok;
+  const int32_t *cu;  // sequence offsets (see above) or NULL
+  int n_cu;           // sequences that cu describes
+  int max_tokens;     // kShared, chunks: host bound of a sequence's tokens (sizes the launch)
+  const int32_t *ctx_lens;
+  const int32_t *prefix_lens;
+  int window, sinks;
+  float scale_log2;  // sm_scale * log2(e)
+  // partial results: slot k of row (token, head) at (token * Hq + head) * slots + k
+  float *o_part;    // [n_tok, Hq, slots, D], normalised
+  float *lse_part;  // [n_tok, Hq, slots]
+  int slots;        // 1: the kernel writes o / lse itself
+  int slot0;        // first slot of this launch
+  int splits;       // slots of this launch
+};
+
+// One sequence of query tokens.
+struct Seq {
+  int tok0, ntok;  // its query tokens are rows tok0 .. tok0 + ntok - 1 of q
+  int table;       // its block-table row
+  int first;       // kWindow / kTail: position of its first query token
+  int prefix;      // kShared / kTail: keys of the shared prefix
+  bool grouped;    // kTail: the request belongs to a group
+};
+
+// Sequence s; a malformed description (offsets that fall or leave the query
+// rows) is recorded and gives an empty sequence.
+template <int MODE>
+__device__ __forceinline__ Seq sequence(const Args &a, int s) {
+  Seq q;
+  q.table = s;
+  q.prefix = 0;
+  q.first = 0;
+  q.grouped = false;
+  if (MODE == kShared) {
+    const int r0 = a.cu[s], r1 = a.cu[s + 1];
+    q.prefix = a.prefix_lens[s];
+    if (r0 < 0 || r1 < r0 || r1 > a.B || q.prefix < 0 || (r1 - r0) * a.T > a.max_tokens) {
+      record_error(kErrBadInput);
+      q.tok0 = q.ntok = 0;
+      return q;
+    }
+    q.tok0 = r0 * a.T;
+    q.ntok = (r1 - r0) * a.T;
+    q.table = r0;
+    return q;
+  }
+  if (MODE == kWindow && a.cu) {
+    const int t0 = a.cu[s], t1 = a.cu[s + 1];
+    if (t0 < 0 || t1 < t0 || t1 > a.n_tok || t1 - t0 > a.max_tokens) {
+      record_error(kErrBadInput);
+      q.tok0 = q.ntok = 0;
+      return q;
+    }
+    q.tok0 = t0;
+    q.ntok = t1 - t0;
+    q.first = a.ctx_lens[s] - q.ntok;
+    return q;
+  }
+  q.tok0 = s * a.T;
+  q.ntok = a.T;
+  q.first = a.ctx_lens[s] - a.T;
+  if (MODE == kTail) {
+    // the group that holds request s: the last one that starts at or before it
+    int lo = 0, hi = a.n_cu;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu[mid] <= s) lo = mid;
+      else hi = mid;
+    }
+    // a request outside every group shares nothing
+    q.grouped = a.cu[lo] <= s && s < a.cu[lo + 1];
+    if (q.grouped) q.prefix = max(a.prefix_lens[lo], 0);
+  }
+  return q;
+}
+
+// Keys the query token `i` (of the sequence) sees: key < hi and (key >= lo
+// or key < sink).
+struct Seen {
+  int hi, lo, sink;
+};
+template <int MODE>
+__device__ __forceinline__ Seen seen_by(const Args &a, const Seq &q, int i) {
+  Seen v;
+  v.sink = 0;
+  v.lo = 0;
+  if (MODE == kShared) {
+    const int tok = q.tok0 + i, r = tok / a.T;
+    v.hi = min(q.prefix, a.ctx_lens[r] - a.T + (tok - r * a.T) + 1);
+    return v;
+  }
+  v.hi = q.first + i + 1;
+  if (MODE == kTail) {
+    v.lo = q.prefix;
+  } else {
+    v.lo = max(0, v.hi - a.window);
+    v.sink = a.sinks;
+  }
+  return v;
+}
+__device__ __forceinline__ bool sees(const Seen &v, int key) {
+  return key < v.hi && (key >= v.lo || key < v.sink);
+}
+
+// The keys that some token of [i0, i1) of the sequence may see, as a virtual
+// range: virtual key x is key x below sa, else b0 + x - sa.
+struct Range {
+  int sa, b0, n;
+  __device__ __forceinline__ int key(int x) const { return x < sa ? x : b0 + (x - sa); }
+};
+template <int MODE>
+__device__ __forceinline__ Range range_of(const Args &a, const Seq &q, int i0, int i1) {
+  Range r;
+  r.sa = r.b0 = r.n = 0;
+  if (i1 <= i0) return r;
+  int lo, hi, sink = 0;
+  if (MODE == kShared) {
+    lo = 0;
+    hi = q.prefix;  // a query before the prefix's end masks what it does not see
+  } else {
+    hi = q.first + i1;
+    lo = MODE == kTail ? q.prefix : max(0, q.first + i0 + 1 - a.window);
+    sink = MODE == kTail ? 0 : a.sinks;
+  }
+  if (hi <= 0) return r;
+  // a length that the block table cannot hold is cut to what it can
+  const long long cap = (long long)a.c.max_pages_per_req * a.c.page_size;
+  if (hi > cap) {
+    record_error(kErrBounds);
+    hi = (int)cap;
+  }
+  sink = (min(sink, hi) + 3) & ~3;
+  lo &= ~3;
+  if (lo >= hi) lo = hi;
+  if (sink >= lo) {  // one range
+    r.sa = 0;
+    r.b0 = sink > 0 ? 0 : lo;
+    r.n = hi - r.b0;
+    return r;
+  }
+  r.sa = sink;
+  r.b0 = lo;
+  r.n = sink + hi - lo;
+  return r;
+}
+
+// Split k of n virtual keys in `splits`: bounds at multiples of `unit`.
+__device__ __forceinline__ int split_bound(int n, int splits, int k, int unit) {
+  const long long units = (n + unit - 1) / unit;
+  return (int)min((long long)n, units * k / splits * unit);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void store4(float *p, const float4 &v) {
+  *reinterpret_cast<float4 *>(p) = v;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 w;
+  w.x = *reinterpret_cast<uint32_t *>(&a);
+  w.y = *reinterpret_cast<uint32_t *>(&b);
+  *reinterpret_cast<uint2 *>(p) = w;
+}
+
+// Merge of the partial results of every (token, head) row, one warp each:
+//   lse = log sum_k exp(lse_k),  o = sum_k exp(lse_k - lse) o_k,
+// o = 0 and lse = -inf for a row that saw nothing.  Slots are added in order,
+// so a result does not depend on how the work was scheduled.
+constexpr int kMergeThreads = 128;
+
+template <int D, typename OutT>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(Args a) {
+  pdl_open();
+  const long long row = ((long long)blockIdx.x * kMergeThreads + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (row >= (long long)a.n_tok * a.Hq) return;
+  if (a.cu && a.prefix_lens == nullptr && row / a.Hq >= a.cu[a.n_cu]) return;  // rows behind the last sequence
+  const int S = a.slots;
+  const float *lp = a.lse_part + row * S;
+  float mx = -INFINITY;
+  for (int k = lane; k < S; k += 32) mx = fmaxf(mx, __ldcg(lp + k));
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float z = 0.f;
+  const int d = 4 * lane;
+  if (mx != -INFINITY) {
+    for (int k = 0; k < S; ++k) {
+      const float l = __ldcg(lp + k);
+      if (l == -INFINITY) continue;
+      const float w = __expf(l - mx);
+      z += w;
+      if (d < D) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.o_part + (row * S + k) * D + d));
+        acc.x = __fmaf_rn(w, v.x, acc.x);
+        acc.y = __fmaf_rn(w, v.y, acc.y);
+        acc.z = __fmaf_rn(w, v.z, acc.z);
+        acc.w = __fmaf_rn(w, v.w, acc.w);
+      }
+    }
+  }
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  acc.x *= inv;
+  acc.y *= inv;
+  acc.z *= inv;
+  acc.w *= inv;
+  if (d < D) store4(static_cast<OutT *>(a.o) + row * D + d, acc);
+  if (lane == 0) a.lse[row] = z > 0.f ? mx + __logf(z) : -INFINITY;
+}
+
+}  // namespace attn
+}  // namespace qsa

@@ -1,0 +1,396 @@
+// Attention of few query rows over key ranges, BF16 and FP8 caches: the decode
+// form of qsa_window_decode and the tails of qsa_prefix_decode.
+//
+// At most 32 query rows (T query tokens x G heads) share a kv head's keys, so
+// the work is a stream of K/V rows at 8 to 32 multiply-adds a byte: HBM bounds
+// it.  Both products put the keys on the wide side of m16n8k16 tiles
+// (S^T = K Q^T, O^T = V^T P^T), so 8 query rows fill a tile.  A CTA of 4 warps
+// takes a split of one (request, kv head); each warp streams a contiguous part
+// of it, 16 keys a stage, through its own cp.async ring with its own running
+// maximum and sum (no barriers while it streams), and the four results are
+// merged in shared memory.  fp8 tiles go from shared memory into f16 fragments
+// (fp8_frag.cuh).
+//
+// Weights p = exp(s - max) enter the value product rounded to bf16 (2^-9
+// relative) or, times the V scale, to f16 (2^-12): o is rounded to bf16 itself.
+#pragma once
+#include "attn_common.cuh"
+#include "sparse_decode_warp.cuh"
+
+namespace qsa {
+namespace attn {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kStageKeys = 16;
+constexpr int kMetaKeys = 128;  // keys whose pages a warp looks up at once: 4 a lane
+
+// Stages of a warp's ring: 96 KB (bf16) or 64 KB (fp8) of shared memory a CTA
+// at D = 128, two and three CTAs an SM.
+template <bool FP8>
+__host__ __device__ constexpr int dec_stages() { return FP8 ? 4 : 3; }
+
+template <int D, bool FP8, int NT>
+struct DecSmem {
+  static constexpr int kRowBytes = D * (FP8 ? 1 : 2);
+  static constexpr int kRing = dec_stages<FP8>() * 2 * kStageKeys * kRowBytes;  // per warp
+  static constexpr int kOut = NT * 8 * D * 4;
+  union {
+    uint8_t ring[kDecWarps][kRing];
+    float o[kDecWarps][NT * 8][D];
+  };
+  float m[kDecWarps][NT * 8], l[kDecWarps][NT * 8];
+};
+
+// Grid (splits, Hkv, requests).
+template <int MODE, int D, bool FP8, int NT>
+__global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Args a) {
+  pdl_open();
+  using namespace qsa::dec;
+  constexpr int NS = dec_stages<FP8>();
+  constexpr int MD = D / 16;
+  constexpr int kRowBytes = D * (FP8 ? 1 : 2);
+  constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks of a row
+  constexpr int kTile = kStageKeys * kRowBytes;
+  constexpr int kRowsPerIssue = 32 / kChunks;      // rows one cp.async of the warp covers
+  using SM = DecSmem<D, FP8, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  SM &sm = *reinterpret_cast<SM *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gq = lane >> 2, cq = lane & 3;
+  const int g = blockIdx.y, split = blockIdx.x, r = blockIdx.z;
+  const Seq sq = sequence<MODE>(a, r);
+  const Range rg = range_of<MODE>(a, sq, 0, a.T);
+  const int x0 = split_bound(rg.n, a.splits, split, kStageKeys);
+  const int x1 = split_bound(rg.n, a.splits, split + 1, kStageKeys);
+  const int M = a.T * a.G, Hkv = a.c.num_kv_heads;
+  const long long row_stride = (long long)Hkv * kRowBytes;  // bytes between tokens
+
+  float o[MD][NT][4], mcol[NT][2], lcol[NT][2];
+#pragma unroll
+  for (int i = 0; i < MD; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    mcol[j][0] = mcol[j][1] = -INFINITY;
+    lcol[j][0] = lcol[j][1] = 0.f;
+  }
+  float vsref = 0.f;  // power of two that the V scales are relative to
+
+  // this warp's part of the split
+  const int w0 = x0 + split_bound(x1 - x0, kDecWarps, warp, kStageKeys);
+  const int w1 = x0 + split_bound(x1 - x0, kDecWarps, warp + 1, kStageKeys);
+  if (w0 < w1) {
+    uint8_t *ring = sm.ring[warp];
+    const uint8_t *kbase = static_cast<const uint8_t *>(a.c.k_cache) + (long long)g * kRowBytes;
+    const uint8_t *vbase = static_cast<const uint8_t *>(a.c.v_cache) + (long long)g * kRowBytes;
+    // ---- pages: lane i holds the first token row of the four keys from
+    // window start + 4 i on (-1: none), and their scales
+    auto lookup = [&](int xw, long long &row, float &ks, float &vs) {
+      const int x = xw + 4 * lane;
+      row = -1;
+      ks = vs = 0.f;
+      if (x < w1) {
+        const int key = rg.key(x);
+        const int lp = key / a.c.page_size;
+        const int pg = physical_page(a.c, sq.table, lp);
+        if (pg >= 0) {
+          row = (long long)pg * a.c.page_size + (key - lp * a.c.page_size);
+          if constexpr (FP8) {
+            ks = a.c.k_scale[(long long)pg * Hkv + g];
+            vs = a.c.v_scale[(long long)pg * Hkv + g];
+          }
+        }
+      }
+    };
+    long long row_cur, row_next;
+    float ks_cur, vs_cur, ks_next, vs_next;
+    lookup(w0, row_cur, ks_cur, vs_cur);
+    int win = w0;  // start of the window held in *_cur
+    lookup(w0 + kMetaKeys, row_next, ks_next, vs_next);
+    // the keys that some query of the request sees are loaded, the others of
+    // a group of four (and past the end) are zero
+    Seen any = seen_by<MODE>(a, sq, a.T - 1);
+    if (MODE == kWindow) any.lo = max(0, sq.first + 1 - a.window);
+    // ---- issue of stage s (keys w0 + 16 s ..) into its slot
+    auto issue = [&](int s) {
+      const int xs = w0 + s * kStageKeys;
+      uint8_t *kt = ring + (s % NS) * 2 * kTile, *vt = kt + kTile;
+      const bool next = xs >= win + kMetaKeys;  // the prefetch is at most one window ahead
+      const int base = (xs - win - (next ? kMetaKeys : 0)) >> 2;
+#pragma unroll
+      for (int i = 0; i < kStageKeys / kRowsPerIssue; ++i) {
+        const int row = i * kRowsPerIssue + lane / kChunks, ch = lane % kChunks;
+        const long long r0 = __shfl_sync(0xffffffffu, next ? row_next : row_cur, base + (row >> 2));
+        const int x = xs + row;
+        const int key = rg.key(x);
+        const bool ok = x < w1 && r0 >= 0 && sees(any, key);
+        const long long at = (r0 + (row & 3)) * row_stride + ch * 16;
+        const int so = FP8 ? fp8_swz<D>(row, ch) : swz<D>(row, ch);
+        cp_async16_zfill(kt + so, ok ? kbase + at : kbase, ok);
+        cp_async16_zfill(vt + so, ok ? vbase + at : vbase, ok);
+      }
+    };
+    const int nst = (w1 - w0 + kStageKeys - 1) / kStageKeys;
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      if (s < nst) issue(s);
+      cp_async_commit();
+    }
+    // ---- Q as B fragments, rows past M zero
+    uint32_t qb[NT][MD][2];
+    float csc[NT][2];
+    int rlo[NT][2], rhi[NT][2], rsink = MODE == kWindow ? a.sinks : 0;
+    int all_lo = 0, all_hi = 0x7fffffff;  // keys in [all_lo, all_hi) are seen by every row
+    const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(a.q);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int m = 8 * j + gq;
+      const __nv_bfloat16 *qrow =
+          m < M ? qg + ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D : nullptr;
+      if constexpr (FP8) {
+        const float sc = q_frags_f16<D>(qrow, cq, qb[j]);
+        csc[j][0] = __shfl_sync(0xffffffffu, sc, 4 * (2 * cq)) * a.scale_log2;
+        csc[j][1] = __shfl_sync(0xffffffffu, sc, 4 * (2 * cq + 1)) * a.scale_log2;
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < MD; ++kk) {
+          qb[j][kk][0] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq) : 0u;
+          qb[j][kk][1] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq + 8) : 0u;
+        }
+        csc[j][0] = csc[j][1] = a.scale_log2;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int mm = 8 * j + 2 * cq + e;
+        rlo[j][e] = rhi[j][e] = 0;
+        if (mm < M) {
+          const Seen v = seen_by<MODE>(a, sq, mm / a.G);
+          rlo[j][e] = v.lo;
+          rhi[j][e] = v.hi;
+        }
+      }
+    }
+    {
+      const Seen first = seen_by<MODE>(a, sq, 0), last = seen_by<MODE>(a, sq, a.T - 1);
+      all_hi = first.hi;
+      all_lo = last.lo;
+    }
+
+    for (int s = 0; s < nst; ++s) {
+      const int xs = w0 + s * kStageKeys;
+      if (xs >= win + kMetaKeys) {  // the next window's pages
+        win += kMetaKeys;
+        row_cur = row_next;
+        ks_cur = ks_next;
+        vs_cur = vs_next;
+        lookup(win + kMetaKeys, row_next, ks_next, vs_next);
+      }
+      if constexpr (FP8) {
+        if (xs == win) {
+          // the window's largest V scale may raise the reference: what is
+          // summed so far goes over to it
+          float mx = fabsf(vs_cur);
+#pragma unroll
+          for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          const float ref = vs_binade(mx);
+          if (mx > 0.f && ref > vsref) {
+            const float f = vsref / ref;
+            vsref = ref;
+#pragma unroll
+            for (int i = 0; i < MD; ++i)
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][j][e] *= f;
+          }
+        }
+      }
+      if (s + NS - 1 < nst) issue(s + NS - 1);
+      cp_async_commit();
+      cp_async_wait<NS - 1>();
+      __syncwarp();
+      const uint8_t *kt = ring + (s % NS) * 2 * kTile, *vt = kt + kTile;
+      // ---- S^T = K Q^T
+      float sacc[NT][4], sac2[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sacc[j][e] = sac2[j][e] = 0.f;
+      if constexpr (FP8) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) qk_fp8<D>(kt, gq, cq, qb[j], sacc[j], sac2[j]);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < MD; ++kk) {
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4(a0, a1, a2, a3, kt + swz<D>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * kk + (lane >> 4)));
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (kk & 1) mma_bf16(sac2[j], a0, a1, a2, a3, qb[j][kk][0], qb[j][kk][1]);
+            else mma_bf16(sacc[j], a0, a1, a2, a3, qb[j][kk][0], qb[j][kk][1]);
+          }
+        }
+      }
+      // ---- softmax; this lane's keys are gq and gq + 8 of the stage
+      const int xk = xs + gq, k0 = rg.key(xk), k1 = rg.key(xk + 8);
+      const int first = rg.key(xs);
+      const bool whole = xs + kStageKeys <= w1 && rg.key(xs + kStageKeys - 1) == first + kStageKeys - 1 &&
+                         first + kStageKeys <= all_hi && (first >= all_lo || first + kStageKeys <= rsink);
+      float f0 = 1.f, f1 = 1.f, v0 = 1.f, v1 = 1.f;
+      if constexpr (FP8) {
+        const int at = (xk - win) >> 2;
+        f0 = __shfl_sync(0xffffffffu, ks_cur, at);
+        f1 = __shfl_sync(0xffffffffu, ks_cur, at + 2);
+        const float inv = vsref > 0.f ? 1.f / vsref : 0.f;
+        v0 = __shfl_sync(0xffffffffu, vs_cur, at) * inv;
+        v1 = __shfl_sync(0xffffffffu, vs_cur, at + 2) * inv;
+      }
+      uint32_t pb[NT][2];
+      float alpha[NT][2];
+      bool rescale = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y0 = (sacc[j][e] + sac2[j][e]) * csc[j][e], y1 = (sacc[j][2 + e] + sac2[j][2 + e]) * csc[j][e];
+          if constexpr (FP8) {
+            y0 *= f0;
+            y1 *= f1;
+          }
+          if (!whole) {
+            const bool in0 = k0 < rhi[j][e] && (k0 >= rlo[j][e] || k0 < rsink) && xk < w1;
+            const bool in1 = k1 < rhi[j][e] && (k1 >= rlo[j][e] || k1 < rsink) && xk + 8 < w1;
+            if (!in0) y0 = -INFINITY;
+            if (!in1) y1 = -INFINITY;
+          }
+          float mx = fmaxf(y0, y1);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float m_new = fmaxf(mcol[j][e], mx);
+          const float base = m_new == -INFINITY ? 0.f : m_new;
+          const float al = m_new == -INFINITY ? 1.f : attn::ex2(mcol[j][e] - base);
+          alpha[j][e] = al;
+          rescale |= al != 1.f;
+          mcol[j][e] = m_new;
+          p[e] = attn::ex2(y0 - base);
+          p[2 + e] = attn::ex2(y1 - base);
+          lcol[j][e] = lcol[j][e] * al + p[e] + p[2 + e];
+        }
+        if constexpr (FP8) {
+          pb[j][0] = movmatrix_t(pack_f16(p[0] * v0, p[1] * v0));
+          pb[j][1] = movmatrix_t(pack_f16(p[2] * v1, p[3] * v1));
+        } else {
+          pb[j][0] = movmatrix_t(pack_bf16(p[0], p[1]));
+          pb[j][1] = movmatrix_t(pack_bf16(p[2], p[3]));
+        }
+      }
+      if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+        for (int i = 0; i < MD; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            o[i][j][0] *= alpha[j][0];
+            o[i][j][1] *= alpha[j][1];
+            o[i][j][2] *= alpha[j][0];
+            o[i][j][3] *= alpha[j][1];
+          }
+      }
+      // ---- O^T += V^T P^T
+      if constexpr (FP8) {
+        VRaw<D> vr;
+        v_raw_fp8<D>(vt, gq, cq, vr);
+#pragma unroll
+        for (int i = 0; i < MD; ++i) {
+          uint32_t a0, a1, a2, a3;
+          v_frag_fp8<D>(vr, i, a0, a1, a2, a3);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_f16(o[i][j], a0, a1, a2, a3, pb[j][0], pb[j][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < MD; ++i) {
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4_t(a0, a1, a2, a3, vt + swz<D>((lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_bf16(o[i][j], a0, a1, a2, a3, pb[j][0], pb[j][1]);
+        }
+      }
+      __syncwarp();  // the slot may be refilled
+    }
+    cp_async_wait<0>();
+  }
+  __syncthreads();  // the rings become the four results
+
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = lcol[j][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int m = 8 * j + 2 * cq + e;
+      float *row = sm.o[warp][m];
+      if constexpr (FP8) {
+        store_col_fp8<D>(row, [&](int i, int k) { return o[i][j][k]; }, e, gq, vsref);
+      } else {
+#pragma unroll
+        for (int i = 0; i < MD; ++i) {
+          row[16 * i + gq] = o[i][j][e];
+          row[16 * i + gq + 8] = o[i][j][2 + e];
+        }
+      }
+      if (gq == 0) {
+        sm.m[warp][m] = mcol[j][e];
+        sm.l[warp][m] = l;
+      }
+    }
+  __syncthreads();
+  constexpr int kVec = D / 4;
+  for (int e = threadIdx.x; e < M * kVec; e += kDecThreads) {
+    const int m = e / kVec, d = e % kVec * 4;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, sm.m[w][m]);
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mx != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float f = attn::ex2(sm.m[w][m] - mx);
+        const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][m][d]);
+        l += f * sm.l[w][m];
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    const long long at = (long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G;
+    const float lse = l > 0.f ? (mx + __log2f(l)) * attn::kLn2 : -INFINITY;
+    if (a.slots > 1) {
+      const long long slot = at * a.slots + a.slot0 + split;
+      if (l > 0.f) store4(a.o_part + slot * D + d, acc);
+      if (d == 0) {
+        a.lse_part[slot] = lse;
+        if (MODE == kTail && split == 0 && !sq.grouped)
+          for (int k = 0; k < a.slot0; ++k) a.lse_part[at * a.slots + k] = -INFINITY;
+      }
+    } else {
+      store4(static_cast<__nv_bfloat16 *>(a.o) + at * D + d, acc);
+      if (d == 0) a.lse[at] = lse;
+    }
+  }
+}
+
+}  // namespace attn
+}  // namespace qsa

@@ -1,0 +1,180 @@
+// Attention over key ranges on the CUDA cores, in float32 throughout: the
+// kernel of float32 caches.
+//
+// One CTA of 4 warps takes a tile of 16 query rows of one sequence and kv
+// head and one split of its keys.  32 keys at a time are staged in shared
+// memory; a lane owns a key for the scores (its row padded against bank
+// conflicts) and a slice of the head dimension for the values, a warp owns 4
+// query rows, and the softmax runs online (running maximum and sum).
+#pragma once
+#include "attn_common.cuh"
+
+namespace qsa {
+namespace attn {
+
+constexpr int kSimpleThreads = 128;
+constexpr int kSimpleRows = 16;
+constexpr int kSimpleKeys = 32;
+
+template <int D>
+struct SimpleSmem {
+  float q[kSimpleRows][D];
+  float k[kSimpleKeys][D + 4];
+  float v[kSimpleKeys][D];
+};
+
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+  const uint2 w = *reinterpret_cast<const uint2 *>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ float4 load4(const __nv_fp8_e4m3 *p) {
+  const __nv_fp8x4_e4m3 w = *reinterpret_cast<const __nv_fp8x4_e4m3 *>(p);
+  return static_cast<float4>(w);
+}
+
+// Grid (row tiles, Hkv * splits, sequences).
+template <int MODE, int D, typename QT, typename KT>
+__global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
+  pdl_open();
+  constexpr int kVec = D / 4;
+  constexpr int kRowsPerWarp = kSimpleRows / 4;
+  constexpr int kDims = D / 32;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SimpleSmem<D> &sm = *reinterpret_cast<SimpleSmem<D> *>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Seq sq = sequence<MODE>(a, blockIdx.z);
+  const int m0 = blockIdx.x * kSimpleRows;
+  const int rows = min(kSimpleRows, sq.ntok * a.G - m0);
+  if (rows <= 0) return;
+  const int g = blockIdx.y / a.splits, split = blockIdx.y - g * a.splits;
+  const Range rg = range_of<MODE>(a, sq, m0 / a.G, (m0 + rows - 1) / a.G + 1);
+  const int x0 = split_bound(rg.n, a.splits, split, kSimpleKeys);
+  const int x1 = split_bound(rg.n, a.splits, split + 1, kSimpleKeys);
+
+  for (int e = tid; e < kSimpleRows * kVec; e += kSimpleThreads) {
+    const int m = e / kVec, d = e % kVec * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m < rows) {
+      const int row = m0 + m;
+      const long long at = ((long long)(sq.tok0 + row / a.G) * a.Hq + g * a.G + row % a.G) * D;
+      v = load4(static_cast<const QT *>(a.q) + at + d);
+    }
+    *reinterpret_cast<float4 *>(&sm.q[m][d]) = v;
+  }
+  Seen see[kRowsPerWarp];
+  float mx[kRowsPerWarp], l[kRowsPerWarp], o[kRowsPerWarp][kDims];
+#pragma unroll
+  for (int j = 0; j < kRowsPerWarp; ++j) {
+    const int m = warp * kRowsPerWarp + j;
+    see[j].hi = see[j].lo = see[j].sink = 0;
+    if (m < rows) see[j] = seen_by<MODE>(a, sq, (m0 + m) / a.G);
+    mx[j] = -INFINITY;
+    l[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDims; ++i) o[j][i] = 0.f;
+  }
+
+  for (int xt = x0; xt < x1; xt += kSimpleKeys) {
+    __syncthreads();  // the tile before is read
+    for (int e = tid; e < kSimpleKeys * kVec; e += kSimpleThreads) {
+      const int j = e / kVec, d = e % kVec * 4, x = xt + j;
+      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+      if (x < x1) {
+        const int key = rg.key(x);
+        const int lp = key / a.c.page_size;
+        const int pg = physical_page(a.c, sq.table, lp);
+        if (pg >= 0) {
+          const long long at =
+              (((long long)pg * a.c.page_size + (key - lp * a.c.page_size)) * a.c.num_kv_heads + g) * D + d;
+          kv = load4(static_cast<const KT *>(a.c.k_cache) + at);
+          vv = load4(static_cast<const KT *>(a.c.v_cache) + at);
+          if (a.c.k_scale) {
+            const float ks = a.c.k_scale[(long long)pg * a.c.num_kv_heads + g];
+            const float vs = a.c.v_scale[(long long)pg * a.c.num_kv_heads + g];
+            kv.x *= ks, kv.y *= ks, kv.z *= ks, kv.w *= ks;
+            vv.x *= vs, vv.y *= vs, vv.z *= vs, vv.w *= vs;
+          }
+        }
+      }
+      *reinterpret_cast<float4 *>(&sm.k[j][d]) = kv;
+      *reinterpret_cast<float4 *>(&sm.v[j][d]) = vv;
+    }
+    __syncthreads();
+    float s[kRowsPerWarp];
+#pragma unroll
+    for (int j = 0; j < kRowsPerWarp; ++j) s[j] = 0.f;
+#pragma unroll 8
+    for (int d = 0; d < D; d += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(&sm.k[lane][d]);
+#pragma unroll
+      for (int j = 0; j < kRowsPerWarp; ++j) {
+        const float4 q = *reinterpret_cast<const float4 *>(&sm.q[warp * kRowsPerWarp + j][d]);
+        s[j] += q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+      }
+    }
+    const int key = rg.key(xt + lane);
+#pragma unroll
+    for (int j = 0; j < kRowsPerWarp; ++j) {
+      const bool ok = xt + lane < x1 && sees(see[j], key);
+      const float x = ok ? s[j] * a.scale_log2 : -INFINITY;
+      float t = x;
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+      const float m_new = fmaxf(mx[j], t);
+      const float base = m_new == -INFINITY ? 0.f : m_new;
+      const float al = m_new == -INFINITY ? 1.f : ex2(mx[j] - base);
+      const float p = ex2(x - base);
+      mx[j] = m_new;
+      l[j] = l[j] * al + p;
+#pragma unroll
+      for (int i = 0; i < kDims; ++i) o[j][i] *= al;
+      s[j] = p;
+    }
+#pragma unroll 4
+    for (int t = 0; t < kSimpleKeys; ++t) {
+      float v[kDims];
+#pragma unroll
+      for (int i = 0; i < kDims; ++i) v[i] = sm.v[t][lane + 32 * i];
+#pragma unroll
+      for (int j = 0; j < kRowsPerWarp; ++j) {
+        const float p = __shfl_sync(0xffffffffu, s[j], t);
+#pragma unroll
+        for (int i = 0; i < kDims; ++i) o[j][i] = p > 0.f ? fmaf(p, v[i], o[j][i]) : o[j][i];
+      }
+    }
+  }
+
+#pragma unroll
+  for (int j = 0; j < kRowsPerWarp; ++j) {
+    const int m = warp * kRowsPerWarp + j;
+    if (m >= rows) continue;
+    float t = l[j];
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    const float inv = t > 0.f ? 1.f / t : 0.f;
+    const float lse = t > 0.f ? (mx[j] + __log2f(t)) * kLn2 : -INFINITY;
+    const int row = m0 + m;
+    const long long at = (long long)(sq.tok0 + row / a.G) * a.Hq + g * a.G + row % a.G;
+    if (a.slots > 1) {
+      const long long slot = at * a.slots + a.slot0 + split;
+      if (lane == 0) a.lse_part[slot] = lse;
+      // a request outside every group: nothing else writes its shared slots
+      if (MODE == kTail && split == 0 && !sq.grouped)
+        for (int k = lane; k < a.slot0; k += 32) a.lse_part[at * a.slots + k] = -INFINITY;
+      if (t > 0.f) {
+#pragma unroll
+        for (int i = 0; i < kDims; ++i) a.o_part[slot * D + lane + 32 * i] = o[j][i] * inv;
+      }
+    } else {
+      if (lane == 0) a.lse[at] = lse;
+#pragma unroll
+      for (int i = 0; i < kDims; ++i)
+        static_cast<QT *>(a.o)[at * D + lane + 32 * i] = static_cast<QT>(o[j][i] * inv);
+    }
+  }
+}
+
+}  // namespace attn
+}  // namespace qsa

@@ -1081,3 +1081,5 @@ qsa_status qsa_index_topk_noalloc(const qsa_cache *cache, int32_t B, const int8_
 }
 
 }  // extern "C"
+
+#include "attn_api.cuh"

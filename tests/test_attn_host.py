@@ -1,0 +1,194 @@
+"""Rotary append, window attention and shared-prefix decode: what the host
+checks before anything is launched, the frequencies, and the workspace sizes.
+No GPU."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from sparse_attention_decode_compress_b200 import QSAError, _lib, qsa_rope_freqs
+
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+P = 1 << 20  # an aligned address that nothing reads: every call below is refused
+
+
+def cache(**kw):
+    s = _lib.QsaCacheStruct()
+    s.num_pages, s.page_size, s.num_kv_heads, s.head_dim, s.idx_dim = 10, 64, 2, 128, 0
+    s.kv_dtype, s.ring_rows, s.max_pages_per_req = _lib.QSA_BF16, 0, 4
+    s.k_cache = s.v_cache = s.block_table = P
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return ctypes.byref(s)
+
+
+# ------------------------------------------------------------ frequencies --
+def test_frequencies_are_the_formula():
+    for R, theta in ((128, 1e6), (64, 1e4), (2, 1e4), (48, 500000.0)):
+        turns, inv, m = qsa_rope_freqs(R, theta)
+        assert m == 1.0 and len(turns) == len(inv) == R // 2
+        for i, (t, f) in enumerate(zip(turns, inv)):
+            assert math.isclose(f, theta ** (-2 * i / R), rel_tol=1e-14)
+            # float64 division, and the cut to whole units of 2^-64 (a slow
+            # pair's fraction has few of them: the error is absolute)
+            assert math.isclose(t / 2 ** 64, f / (2 * math.pi), rel_tol=1e-14, abs_tol=2.0 ** -64)
+
+
+def test_scaled_frequencies():
+    R, theta, s = 64, 1e4, 4.0
+    plain = qsa_rope_freqs(R, theta)[1]
+    _, lin, m = qsa_rope_freqs(R, theta, "linear", s)
+    assert m == 1.0 and all(math.isclose(a, b / s, rel_tol=1e-14) for a, b in zip(lin, plain))
+    _, ntk, m = qsa_rope_freqs(R, theta, "ntk", s)
+    # the fastest pair is unchanged, the slowest is stretched by the factor
+    assert m == 1.0 and ntk[0] == 1.0 and math.isclose(ntk[-1], plain[-1] / s, rel_tol=1e-12)
+    _, yarn, m = qsa_rope_freqs(R, theta, "yarn", s, 4096)
+    assert math.isclose(m, 0.1 * math.log(s) + 1, rel_tol=1e-6)
+    for a, b in zip(yarn, plain):
+        turns = 4096 * b / (2 * math.pi)
+        assert b / s * (1 - 1e-12) <= a <= b * (1 + 1e-12)
+        if turns > 64:
+            assert a == b
+        if turns < 0.5:
+            assert math.isclose(a, b / s, rel_tol=1e-14)
+    assert all(x >= y for x, y in zip(yarn, yarn[1:]))
+
+
+def test_whole_turns_fall_away():
+    # a position's angle is freqs * position modulo one turn, however far
+    turns, inv, _ = qsa_rope_freqs(64, 1e6)
+    for t, f in zip(turns, inv):
+        for p in (1, 1000, 2 ** 31 - 1):
+            want = math.fmod(p * f / (2 * math.pi), 1.0)
+            got = (p * t % 2 ** 64) / 2 ** 64
+            d = abs(got - want)
+            # p units of 2^-64, and float64's rounding of the turns themselves
+            assert min(d, 1 - d) < p * 2.0 ** -64 + 2.0 ** -50 * max(1.0, p * f)
+
+
+@pytest.mark.parametrize("kw", [dict(rotary_dim=3), dict(rotary_dim=-2), dict(rotary_dim=130),
+                                dict(rotary_dim=64, theta=1.0), dict(rotary_dim=64, theta=math.nan),
+                                dict(rotary_dim=64, theta=math.inf),
+                                dict(rotary_dim=64, scaling="linear", factor=0.5),
+                                dict(rotary_dim=2, scaling="ntk", factor=2.0),
+                                dict(rotary_dim=64, scaling="yarn", factor=2.0),
+                                dict(rotary_dim=64, scaling="yarn", factor=2.0, original_max_position=64,
+                                     beta_slow=0.0),
+                                dict(rotary_dim=64, scaling="yarn", factor=2.0, original_max_position=64,
+                                     beta_fast=0.5)])
+def test_frequency_refusals(kw):
+    with pytest.raises(QSAError):
+        qsa_rope_freqs(**kw)
+
+
+def test_unknown_scaling():
+    with pytest.raises(ValueError):
+        qsa_rope_freqs(64, scaling="other")
+
+
+# ---------------------------------------------------------------- refusals --
+def rope(c=None, B=2, n=4, pos0=P, cu=P, q=P, qs=2048, k=P, ks=256, v=P, vs=256, dt=_lib.QSA_BF16, Hq=16,
+         freqs=P, R=128, layout=0, m=1.0, out=2 * P):
+    return _lib.load().qsa_rope_append(c or cache(), B, n, pos0, cu, q, qs, k, ks, v, vs, dt, Hq, freqs, R,
+                                       layout, m, out, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(B=-1), INVALID), (dict(n=-1), INVALID), (dict(Hq=0), INVALID), (dict(R=3), INVALID),
+    (dict(R=130), INVALID), (dict(R=-2), INVALID), (dict(layout=2), INVALID), (dict(m=math.nan), INVALID),
+    (dict(pos0=None), INVALID), (dict(cu=None), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
+    (dict(v=None), INVALID), (dict(out=None), INVALID), (dict(freqs=None), INVALID),
+    (dict(q=P + 1), INVALID), (dict(freqs=P + 4), INVALID), (dict(qs=2047), INVALID), (dict(ks=255), INVALID),
+    (dict(vs=0), INVALID), (dict(out=P, qs=4096), INVALID), (dict(dt=_lib.QSA_F32), UNSUPPORTED),
+    (dict(c=cache(head_dim=96), R=64), UNSUPPORTED), (dict(c=cache(kv_dtype=7)), UNSUPPORTED),
+    (dict(c=cache(kv_dtype=_lib.QSA_F32)), UNSUPPORTED), (dict(c=cache(kv_dtype=_lib.QSA_FP8_E4M3)), INVALID),
+    (dict(c=cache(k_cache=None)), INVALID), (dict(c=cache(page_size=6)), INVALID),
+    (dict(c=cache(block_table=None)), INVALID), (dict(B=0), OK), (dict(n=0), OK)])
+def test_rope_append_refusals(kw, want):
+    assert rope(**kw) == want
+
+
+def window(c=None, B=2, T=1, Hq=16, q=P, dt=_lib.QSA_BF16, ctx=P, W=64, S=4, scale=1.0, o=P, lse=P, ws=P,
+           nws=1 << 40):
+    return _lib.load().qsa_window_decode(c or cache(), B, T, Hq, q, dt, ctx, W, S, scale, o, lse, ws, nws, None)
+
+
+def chunk(c=None, B=2, n=8, mq=8, cu=P, ctx=P, q=P, dt=_lib.QSA_BF16, Hq=16, W=64, S=4, scale=1.0, o=P, lse=P,
+          ws=P, nws=1 << 40):
+    return _lib.load().qsa_window_prefill(c or cache(), B, n, mq, cu, ctx, q, dt, Hq, W, S, scale, o, lse, ws,
+                                          nws, None)
+
+
+def prefix(c=None, B=2, T=1, Hq=16, q=P, dt=_lib.QSA_BF16, ctx=P, ng=1, cu=P, pl=P, mg=2, mp=64, mt=64, scale=1.0,
+           o=P, lse=P, ws=P, nws=1 << 40):
+    return _lib.load().qsa_prefix_decode(c or cache(), B, T, Hq, q, dt, ctx, ng, cu, pl, mg, mp, mt, scale, o, lse,
+                                         ws, nws, None)
+
+
+COMMON = [(dict(B=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hq=15), INVALID), (dict(scale=0.0), INVALID),
+          (dict(scale=math.inf), INVALID), (dict(q=None), INVALID), (dict(q=P + 2), INVALID),
+          (dict(ctx=None), INVALID), (dict(o=None), INVALID), (dict(o=P + 8), INVALID), (dict(lse=None), INVALID),
+          (dict(dt=_lib.QSA_F32), UNSUPPORTED), (dict(c=cache(kv_dtype=_lib.QSA_F32)), UNSUPPORTED),
+          (dict(c=cache(kv_dtype=_lib.QSA_FP8_E4M3)), INVALID), (dict(c=cache(head_dim=32)), UNSUPPORTED),
+          (dict(c=cache(v_cache=P + 8)), INVALID), (dict(c=cache(page_size=2)), INVALID),
+          (dict(c=cache(max_pages_per_req=0)), INVALID), (dict(B=65536), UNSUPPORTED), (dict(Hq=128), UNSUPPORTED),
+          (dict(B=0), OK)]
+
+
+@pytest.mark.parametrize("kw,want", COMMON + [
+    (dict(T=0), INVALID), (dict(T=5), UNSUPPORTED), (dict(T=4, Hq=32), UNSUPPORTED), (dict(W=0), INVALID),
+    (dict(S=-1), INVALID), (dict(W=1 << 20, c=cache(max_pages_per_req=400), ws=None), INVALID),
+    (dict(W=1 << 20, c=cache(max_pages_per_req=400), nws=100), INVALID),
+    (dict(W=1 << 20, c=cache(max_pages_per_req=400), ws=P + 16), INVALID)])
+def test_window_decode_refusals(kw, want):
+    assert window(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", COMMON + [
+    (dict(n=-1), INVALID), (dict(mq=-1), INVALID), (dict(W=0), INVALID), (dict(S=-1), INVALID),
+    (dict(cu=None), INVALID), (dict(n=0), OK), (dict(mq=0), OK)])
+def test_window_prefill_refusals(kw, want):
+    assert chunk(**kw) == want
+
+
+@pytest.mark.parametrize("kw,want", COMMON + [
+    (dict(T=0), INVALID), (dict(T=5), UNSUPPORTED), (dict(ng=0), INVALID), (dict(ng=3), INVALID),
+    (dict(mg=0), INVALID), (dict(mg=3), INVALID), (dict(mp=-1), INVALID), (dict(mt=-1), INVALID),
+    (dict(cu=None), INVALID), (dict(pl=None), INVALID), (dict(ws=None), INVALID), (dict(nws=16), INVALID),
+    (dict(ws=P + 16), INVALID)])
+def test_prefix_decode_refusals(kw, want):
+    assert prefix(**kw) == want
+
+
+# --------------------------------------------------------------- workspace --
+def test_workspace_bytes():
+    lib = _lib.load()
+    big = cache(max_pages_per_req=4096)
+    w = lib.qsa_window_decode_workspace_bytes
+    # no key range to split: none needed, and none for malformed arguments
+    assert w(big, 300, 1, 16, 16, 0) == 0
+    for bad in ((0, 1, 16, 64, 0), (2, 0, 16, 64, 0), (2, 1, 15, 64, 0), (2, 1, 16, 0, 0), (2, 1, 16, 64, -1)):
+        assert w(big, *bad) == 0
+    # one slot takes D + 1 floats of every (token, head) row
+    n = w(big, 1, 1, 16, 1 << 20, 0)
+    assert n > 0 and n % 256 == 0
+    # a window wider than the block table holds needs no more than the table
+    assert w(big, 1, 1, 16, 2 ** 31 - 1, 2 ** 31 - 1) == w(big, 1, 1, 16, 4096 * 64, 0)
+    p = lib.qsa_prefix_decode_workspace_bytes
+    assert p(big, 32, 1, 16, 1, 32, 4096, 100) >= 2 * 32 * 16 * 129 * 4
+    for bad in ((32, 1, 16, 0, 32, 64, 64), (32, 1, 16, 33, 32, 64, 64), (32, 1, 16, 1, 0, 64, 64),
+                (32, 1, 16, 1, 33, 64, 64), (32, 1, 16, 1, 32, -1, 64), (32, 1, 16, 1, 32, 64, -1)):
+        assert p(big, *bad) == 0
+    assert lib.qsa_window_prefill_workspace_bytes(big, 0, 8, 8, 16, 64, 0) == 0
+
+
+# ----------------------------------------------------------------- binding --
+def test_binding_refuses_host_tensors_and_wrong_types():
+    from sparse_attention_decode_compress_b200 import QSACache, QSARopeAppend, QSAWindowDecode
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    c = QSACache.allocate(k, k.clone(), torch.zeros((2, 2), dtype=torch.int32), 32, 2)
+    with pytest.raises(ValueError):
+        QSAWindowDecode(c, 2, 1, 4, 16)
+    with pytest.raises(ValueError):
+        QSARopeAppend(c, 4, rotary_dim=66)

@@ -1,0 +1,468 @@
+"""Rotary append, window attention and shared-prefix decode on the GPU against
+their plain float64 forms (tests/attn_oracle.py), at the sizes and masks where
+they can go wrong."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attn_oracle as A
+from sparse_attention_decode_compress_b200 import (QSAPrefixDecode, QSARopeAppend, QSAWindowDecode,
+                                                   QSAWindowPrefill, qsa_get_device_error, qsa_rope_append)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _cuda_and_cleanup():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    yield
+    torch.cuda.synchronize()
+    assert qsa_get_device_error() == (0, 0)
+    torch.cuda.empty_cache()
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def queries(shape, kv, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(torch.float32 if kv == "f32" else torch.bfloat16)
+
+
+# ------------------------------------------------------------------ window --
+def window_want(kv, q, lens, T, window, sinks):
+    """Per request rows; also the keys each request reads."""
+    rows, seen = [], {}
+    for r, L in enumerate(lens):
+        toks = []
+        seen[r] = set()
+        for t in range(T):
+            keys = A.visible(L - T + t, window, sinks)
+            seen[r] |= set(keys)
+            toks.append(A.attend(q[r, t], kv.values("k", r, keys), kv.values("v", r, keys), kv.D ** -0.5))
+        rows.append(A.stack(toks))
+    return A.stack(rows), seen
+
+
+WINDOW = [
+    # kv, Hq, Hkv, D, T, page, window, sinks, lens
+    ("f32", 8, 1, 64, 1, 16, 100, 4, [1, 2, 99, 100, 101, 104, 105, 400, 0]),
+    ("f32", 4, 4, 128, 3, 4, 33, 0, [3, 35, 36, 37, 2, 1, 0, 70]),
+    ("bf16", 16, 2, 128, 1, 64, 256, 64, [1, 63, 64, 65, 255, 256, 257, 320, 321, 1000, 0]),
+    ("bf16", 16, 2, 128, 4, 64, 130, 5, [4, 5, 134, 135, 700, 3, 0, 64]),
+    ("bf16", 12, 4, 64, 2, 20, 47, 1, [2, 47, 48, 49, 333, 61]),
+    ("bf16", 8, 8, 128, 1, 16, 1, 0, [1, 2, 17, 300]),
+    ("bf16", 8, 8, 64, 1, 12, 1, 3, [1, 2, 3, 4, 5, 300]),
+    ("bf16", 32, 4, 128, 4, 128, 500, 101, [4, 100, 101, 102, 600, 601, 605, 1200]),
+    ("bf16", 32, 1, 128, 1, 36, 64, 16, [1, 64, 80, 81, 200]),
+    ("bf16", 16, 2, 128, 1, 64, 2 ** 31 - 1, 0, [1, 777, 2100]),
+    ("bf16", 16, 2, 128, 1, 16, 8, 2 ** 31 - 1, [1, 50, 333]),
+    ("e4m3", 32, 4, 128, 1, 64, 200, 16, [1, 16, 199, 200, 201, 216, 217, 1000, 0]),
+    ("e4m3", 16, 2, 64, 4, 16, 77, 4, [4, 76, 77, 80, 81, 82, 500]),
+    ("e4m3", 12, 4, 128, 2, 8, 50, 0, [2, 3, 50, 51, 52, 53, 210]),
+]
+
+
+@pytest.mark.parametrize("kv,Hq,Hkv,D,T,page,window,sinks,lens", WINDOW)
+def test_window_decode(kv, Hq, Hkv, D, T, page, window, sinks, lens):
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=page + T)
+    q = queries((len(lens), T, Hq, D), kv, 3)
+    want, seen = window_want(c, q, lens, T, window, sinks)
+    c.poison(seen)   # what no query sees is NaN,
+    c.unmap(seen)    # and its pages are gone
+    op = QSAWindowDecode(c.cache(), len(lens), T, Hq, window, sinks)
+    o, lse = op(q.cuda(), ints(lens))
+    A.check(o, lse, want, kv, D, "window")
+
+
+@pytest.mark.parametrize("kv,page", [("bf16", 64), ("e4m3", 16), ("f32", 16)])
+def test_window_decode_long_few_requests(kv, page):
+    """One and two requests: the keys are split over many CTAs."""
+    for lens, window, sinks in (([9001], 8000, 64), ([5000, 37], 4096, 4)):
+        c = A.PagedKV(lens, 2, 128, kv, page, "cuda", seed=11)
+        q = queries((len(lens), 1, 16, 128), kv, 4)
+        want, seen = window_want(c, q, lens, 1, window, sinks)
+        c.poison(seen)
+        op = QSAWindowDecode(c.cache(), len(lens), 1, 16, window, sinks)
+        o, lse = op(q.cuda(), ints(lens))
+        A.check(o, lse, want, kv, 128, "window")
+
+
+def test_window_decode_sharp_and_flat_logits():
+    """Logits in the hundreds, all equal, and falling along the keys (the
+    running maximum never moves, or moves at every step)."""
+    lens = [700, 700, 700]
+    c = A.PagedKV(lens, 2, 128, "bf16", 64, "cuda", seed=21)
+    q = queries((3, 1, 16, 128), "bf16", 5)
+    q[0] *= 40
+    q[1] = 0
+    for t in range(700):
+        c.k[c.table_host[2, t // 64], t % 64, :, 0] = float(t) / 4
+    q[2, ..., 0] = 8
+    want, seen = window_want(c, q, lens, 1, 600, 8)
+    o, lse = QSAWindowDecode(c.cache(), 3, 1, 16, 600, 8)(q.cuda(), ints(lens))
+    A.check(o, lse, want, "bf16", 128, "sharp")
+
+
+def test_window_decode_masked_rows_need_no_finite_keys():
+    """Keys with infinite logits that only some query tokens see."""
+    lens = [100]
+    c = A.PagedKV(lens, 1, 64, "bf16", 16, "cuda", seed=22)
+    q = queries((1, 2, 4, 64), "bf16", 6)
+    c.k[c.table_host[0, 99 // 16], 99 % 16] = -3e38  # seen by token 1 only: logits of +-inf
+    want, _ = window_want(c, q, lens, 2, 2 ** 31 - 1, 0)
+    o, lse = QSAWindowDecode(c.cache(), 1, 2, 4, 2 ** 31 - 1)(q.cuda(), ints(lens))
+    first = tuple(x[:, 0] for x in want)
+    A.check(o[:, 0], lse[:, 0], first, "bf16", 64, "the token that does not see it")
+
+
+# ------------------------------------------------------------------- chunk --
+def chunk_want(c, q, new, lens, window, sinks):
+    rows, seen, at = [], {}, 0
+    for r, (m, L) in enumerate(zip(new, lens)):
+        seen[r] = set()
+        for j in range(m):
+            keys = A.visible(L - m + j, window, sinks)
+            seen[r] |= set(keys)
+            rows.append(A.attend(q[at + j], c.values("k", r, keys), c.values("v", r, keys), c.D ** -0.5))
+        at += m
+    return A.stack(rows), seen
+
+
+CHUNK = [
+    # kv, Hq, Hkv, D, page, window, sinks, new, lens
+    ("f32", 8, 1, 64, 16, 40, 4, [1, 17, 0, 33], [1, 60, 5, 200]),
+    ("bf16", 16, 2, 128, 64, 256, 64, [1, 5, 130, 64, 0], [1, 300, 130, 1000, 0]),
+    ("bf16", 16, 2, 128, 64, 2 ** 31 - 1, 0, [200, 33], [200, 700]),
+    ("bf16", 16, 2, 128, 16, 100, 5, [257, 31], [257, 600]),
+    ("bf16", 12, 4, 64, 20, 47, 1, [90, 41, 7], [90, 300, 1001]),
+    ("bf16", 8, 8, 128, 16, 1, 0, [150], [170]),
+    ("bf16", 32, 1, 64, 36, 64, 16, [45, 3], [45, 500]),
+    ("bf16", 8, 8, 64, 128, 300, 130, [300], [700]),
+    ("e4m3", 32, 4, 128, 64, 200, 16, [70, 33, 1], [70, 500, 333]),
+    ("e4m3", 12, 4, 64, 8, 61, 3, [150, 20], [160, 400]),
+    ("e4m3", 16, 2, 128, 20, 128, 0, [129], [640]),
+]
+
+
+@pytest.mark.parametrize("kv,Hq,Hkv,D,page,window,sinks,new,lens", CHUNK)
+def test_window_prefill(kv, Hq, Hkv, D, page, window, sinks, new, lens):
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=page)
+    n = sum(new)
+    q = queries((n, Hq, D), kv, 7)
+    want, seen = chunk_want(c, q, new, lens, window, sinks)
+    c.poison(seen)
+    c.unmap(seen)
+    pad = 3  # rows behind the last request
+    qp = torch.cat([q, queries((pad, Hq, D), kv, 8)]).cuda()
+    op = QSAWindowPrefill(c.cache(), len(lens), n + pad, max(new), Hq, window, sinks)
+    op.o.fill_(7.0)
+    op.lse.fill_(5.0)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    o, lse = op(qp, ints(cu), ints(lens))
+    A.check(o[:n], lse[:n], want, kv, D, "chunk")
+    assert (o[n:] == 7).all() and (lse[n:] == 5).all(), "rows behind the last request changed"
+
+
+def test_window_prefill_is_the_decode_of_its_last_token():
+    """The chunk's rows and the decode call agree (same numbers to rounding)."""
+    lens, new = [500, 300], [20, 20]
+    c = A.PagedKV(lens, 2, 128, "bf16", 64, "cuda", seed=31)
+    q = queries((40, 16, 128), "bf16", 9)
+    cache = c.cache()
+    o, lse = QSAWindowPrefill(cache, 2, 40, 20, 16, 128, 4)(q.cuda(), ints([0, 20, 40]), ints(lens))
+    qd = torch.stack([q[16:20], q[36:40]]).cuda()
+    od, ld = QSAWindowDecode(cache, 2, 4, 16, 128, 4)(qd, ints(lens))
+    assert torch.allclose(lse.view(2, 20, 16)[:, 16:], ld, atol=2e-5)
+    assert torch.allclose(o.view(2, 20, 16, 128)[:, 16:].float(), od.float(), atol=3e-2)
+
+
+# ------------------------------------------------------------------ prefix --
+def prefix_want(c, q, lens, T):
+    rows = []
+    for r, L in enumerate(lens):
+        toks = []
+        for t in range(T):
+            keys = A.visible(L - T + t, 2 ** 31 - 1, 0)
+            toks.append(A.attend(q[r, t], c.values("k", r, keys), c.values("v", r, keys), c.D ** -0.5))
+        rows.append(A.stack(toks))
+    return A.stack(rows)
+
+
+PREFIX = [
+    # kv, Hq, Hkv, D, T, page, groups (prefix pages, extra prefix tokens, tails)
+    ("f32", 8, 1, 64, 1, 16, [(5, 0, [1, 7, 40]), (0, 0, [9, 3])]),
+    ("f32", 4, 4, 128, 2, 4, [(10, 0, [2, 3])]),
+    ("bf16", 16, 2, 128, 1, 64, [(8, 0, [1, 2, 63, 64, 65, 500])]),
+    ("bf16", 16, 2, 128, 1, 64, [(3, 0, [5] * 40), (1, 0, [9]), (20, 0, [100, 1])]),
+    ("bf16", 16, 2, 128, 4, 16, [(7, 0, [4, 5, 90]), (2, 0, [4] * 17)]),
+    ("bf16", 12, 4, 64, 2, 20, [(11, 0, [2, 33, 21])]),
+    ("bf16", 8, 8, 128, 1, 64, [(6, 0, [3] * 33)]),
+    ("bf16", 32, 1, 128, 1, 128, [(4, 0, [17, 200])]),
+    ("e4m3", 32, 4, 128, 1, 64, [(9, 0, [1, 65, 130]), (2, 0, [40] * 5)]),
+    ("e4m3", 16, 2, 64, 4, 16, [(13, 0, [4, 50]), (0, 0, [6])]),
+    ("e4m3", 12, 4, 128, 2, 8, [(30, 0, [2] * 20)]),
+]
+
+
+@pytest.mark.parametrize("kv,Hq,Hkv,D,T,page,groups", PREFIX)
+def test_prefix_decode(kv, Hq, Hkv, D, T, page, groups):
+    lens, share, cu, pre = [], {}, [0], []
+    for pages, extra, tails in groups:
+        first = len(lens)
+        for i, t in enumerate(tails):
+            if i:
+                share[len(lens)] = (first, pages)
+            lens.append(pages * page + t)
+        cu.append(len(lens))
+        pre.append(pages * page)
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=page + T, share=share)
+    q = queries((len(lens), T, Hq, D), kv, 12)
+    want = prefix_want(c, q, lens, T)
+    c.poison({r: range(L) for r, L in enumerate(lens)})
+    op = QSAPrefixDecode(c.cache(), len(lens), T, Hq, len(groups), max_group=max(len(g[2]) for g in groups),
+                         max_prefix=max(pre), max_tail=max(max(g[2]) for g in groups))
+    o, lse = op(q.cuda(), ints(lens), ints(cu), ints(pre))
+    A.check(o, lse, want, kv, D, "prefix")
+
+
+def test_prefix_decode_unaligned_prefix_ungrouped_and_padding_rows():
+    """A prefix that ends inside a page, a prefix longer than a request's
+    context, an empty group, requests before and behind all groups, and a
+    padding row; the host bounds of the lengths are too small on purpose."""
+    page, T, Hq, Hkv, D = 16, 2, 16, 2, 128
+    lens = [20, 90, 101, 75, 33, 0]
+    c = A.PagedKV(lens, Hkv, D, "bf16", page, "cuda", seed=41, share={2: (1, 5), 3: (1, 4)})
+    # requests 1..3 share 77 keys; the page the prefix ends in is a copy
+    for r in (2, 3):
+        for t in range(64, min(77, lens[r])):
+            a, b = (int(c.table_host[x, t // page]) for x in (1, r))
+            for kv in (c.k, c.v):
+                kv[b, t % page] = kv[a, t % page]
+    q = queries((6, T, Hq, D), "bf16", 13)
+    want = prefix_want(c, q, lens, T)
+    op = QSAPrefixDecode(c.cache(), 6, T, Hq, 2, max_group=3, max_prefix=8, max_tail=1)
+    o, lse = op(q.cuda(), ints(lens), ints([1, 4, 4]), ints([77, 50]))
+    A.check(o, lse, want, "bf16", D, "prefix")
+
+
+# -------------------------------------------------------------------- rope --
+ROPE = [
+    # kv, Hq, Hkv, D, page, R, interleaved, scaling, factor, fused
+    ("bf16", 16, 2, 128, 64, 128, False, "none", 1.0, True),
+    ("bf16", 16, 2, 128, 64, 64, True, "yarn", 4.0, False),
+    ("bf16", 12, 4, 64, 20, 48, False, "linear", 8.0, True),
+    ("bf16", 3, 1, 64, 4, 30, True, "ntk", 2.0, True),
+    ("bf16", 8, 8, 128, 16, 0, False, "none", 1.0, False),
+    ("bf16", 32, 4, 128, 64, 128, True, "none", 1.0, False),
+    ("f32", 8, 1, 64, 16, 64, False, "none", 1.0, True),
+    ("f32", 8, 8, 128, 16, 80, True, "yarn", 2.5, False),
+    ("e4m3", 16, 2, 128, 64, 128, False, "none", 1.0, True),
+    ("e4m3", 4, 4, 64, 8, 22, True, "linear", 2.0, False),
+]
+
+
+@pytest.mark.parametrize("kv,Hq,Hkv,D,page,R,interleaved,scaling,factor,fused", ROPE)
+@pytest.mark.parametrize("new,pos0", [([1, 1, 1], [0, 5, 130]), ([7, 0, 40, 1], [0, 3, 25, 99]),
+                                      ([300] + [1] * 40, [10] + list(range(40)))])
+def test_rope_append(kv, Hq, Hkv, D, page, R, interleaved, scaling, factor, fused, new, pos0):
+    lens = [p + n for p, n in zip(pos0, new)]
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=R + page)
+    n, pad = sum(new), 2
+    dt = torch.float32 if kv == "f32" else torch.bfloat16
+    if fused:
+        qkv = queries((n + pad, Hq + 2 * Hkv, D), kv, 14)
+        parts = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        dev = qkv.cuda()
+        dparts = dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:]
+    else:
+        parts = [queries((n + pad, h, D), kv, 15 + i) for i, h in enumerate((Hq, Hkv, Hkv))]
+        dparts = [x.cuda() for x in parts]
+    cache = c.cache()
+    op = QSARopeAppend(cache, Hq, R, 10000.0, interleaved, scaling, factor, original_max_position=64)
+    q_out = torch.full((n + pad, Hq, D), 9.0, dtype=dt, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    op(ints(pos0), ints(cu), *dparts, q_out)
+    got_k, got_v = cache.k_cache.float().double().cpu(), cache.v_cache.float().double().cpu()
+    want_k, want_v = c.k.float().double(), c.v.float().double()
+    assert (q_out[n:] == 9).all(), "rows behind the last request changed"
+    # half a step of the output type, and of the float32 products and angles:
+    # 3 roundings of 2^-24 and an angle of 2^-24 half turns, sincospif to 2^-22
+    half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "e4m3": 2.0 ** -4}
+    at = 0
+    touched = torch.zeros(c.k.shape[:2], dtype=torch.bool)
+    for r, m in enumerate(new):
+        for j in range(m):
+            p = pos0[r] + j
+            pg, off = int(c.table_host[r, p // page]), p % page
+            touched[pg, off] = True
+            for x, got, typ, sc in ((parts[0][at], q_out[at].double().cpu(), "f32" if kv == "f32" else "bf16", None),
+                                    (parts[1][at], got_k[pg, off], kv, c.k_scale)):
+                y, mag = A.rope_row(x, p, op.inv_freq, op.mscale, R, interleaved)
+                if R == 0:
+                    mag = y.abs()
+                e = mag * 2.0 ** -20
+                s = 1.0 if sc is None or typ != "e4m3" else sc[pg].double()[:, None]
+                y, e = y / s, e / s
+                if typ == "e4m3":
+                    y = y.clamp(-448, 448)
+                    e = e + 2.0 ** -10  # half the smallest step, and the division
+                err = (got - y).abs()
+                assert (err <= half[typ] * (y.abs() + e) + e).all(), (r, j, float(err.max()))
+            if kv == "e4m3":
+                y = (parts[2][at].float() / c.v_scale[pg][:, None]).to(torch.float8_e4m3fn).float().double()
+                y = torch.where(y.isnan(), torch.sign(parts[2][at].double()) * 448, y)
+            else:
+                y = parts[2][at].double()
+            assert torch.equal(got_v[pg, off], y)
+            at += 1
+    assert torch.equal(got_k[~touched], want_k[~touched]) and torch.equal(got_v[~touched], want_v[~touched])
+
+
+def test_rope_far_positions_and_in_place():
+    """Angles at positions around two billion, and q rotated in place."""
+    page, D = 64, 128
+    pos = [2 ** 31 - 70, 1048575, 123456789]
+    table = torch.full((3, (2 ** 31 - 1) // page + 1), -1, dtype=torch.int32, device="cuda")
+    for r, p in enumerate(pos):
+        table[r, p // page] = r
+    from sparse_attention_decode_compress_b200 import QSACache
+    kc, vc = (torch.zeros((3, page, 1, D), device="cuda") for _ in range(2))
+    cache = QSACache.allocate(kc, vc, table, 32, 3)
+    q, k, v = (queries((3, h, D), "f32", 20 + h).cuda() for h in (2, 1, 1))
+    op = QSARopeAppend(cache, 2, theta=1e6)
+    keep = q.clone()
+    out = op(ints(pos), ints([0, 1, 2, 3]), q, k, v, q)
+    assert out is q
+    for r, p in enumerate(pos):
+        for got, x in ((q[r], keep[r]), (kc[r, p % page], k[r])):
+            y, mag = A.rope_row(x.cpu(), p, op.inv_freq, 1.0, D, False)
+            # the reference's own angle: p * f in float64, 2^-53 relative, and
+            # the frequency's rounding there
+            e = mag * (2.0 ** -20 + 2.0 ** -51 * p)
+            assert ((got.double().cpu() - y).abs() <= e).all()
+
+
+# ---------------------------------------------------------------- together --
+def test_append_then_attend_then_share():
+    """A serving loop: a prompt is appended and attended as a chunk, two
+    requests continue behind it token by token, and the shared-prefix decode
+    gives what the dense decode of each gives."""
+    Hq, Hkv, D, page = 16, 2, 128, 64
+    P = 256  # prompt
+    c = A.PagedKV([P + 70, P + 70], Hkv, D, "bf16", page, "cuda", seed=51, share={1: (0, P // page)})
+    c.k.zero_()
+    c.v.zero_()
+    cache = c.cache()
+    rope = QSARopeAppend(cache, Hq, theta=1e6)
+    qkv = queries((P, Hq + 2 * Hkv, D), "bf16", 52).cuda()
+    q = rope(ints([0]), ints([0, P]), qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:])
+    chunk = QSAWindowPrefill(cache, 1, P, P, Hq, 2 ** 31 - 1)
+    o, lse = chunk(q, ints([0, P]), ints([P]))
+    c.k, c.v = cache.k_cache.cpu(), cache.v_cache.cpu()
+    want, _ = chunk_want(c, q.cpu(), [P], [P], 2 ** 31 - 1, 0)
+    A.check(o, lse, want, "bf16", D, "prompt")
+    dense = QSAWindowDecode(cache, 2, 1, Hq, 2 ** 31 - 1)
+    shared = QSAPrefixDecode(cache, 2, 1, Hq, 1, 2, P, 70)
+    for step in range(66):
+        qkv = queries((2, Hq + 2 * Hkv, D), "bf16", 100 + step).cuda()
+        q = rope(ints([P + step] * 2), ints([0, 1, 2]), qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:])
+        q = q.view(2, 1, Hq, D)
+        L = ints([P + step + 1] * 2)
+        o, lse = shared(q, L, ints([0, 2]), ints([P]))
+        o2, lse2 = dense(q, L)
+        assert torch.allclose(lse, lse2, atol=2e-5)
+        if step in (0, 63, 65):
+            c.k, c.v = cache.k_cache.cpu(), cache.v_cache.cpu()
+            want = prefix_want(c, q.cpu(), [P + step + 1] * 2, 1)
+            A.check(o, lse, want, "bf16", D, "shared")
+            A.check(o2, lse2, want, "bf16", D, "dense")
+
+
+def test_captured_and_replayed_on_another_stream():
+    """All calls captured into one graph with device lengths that grow."""
+    Hq, Hkv, D, page, B = 16, 2, 128, 64, 3
+    lens = [200, 131, 64]
+    c = A.PagedKV([n + 8 for n in lens], Hkv, D, "bf16", page, "cuda", seed=61)
+    cache = c.cache()
+    rope = QSARopeAppend(cache, Hq)
+    win = QSAWindowDecode(cache, B, 1, Hq, 100, 4)
+    pre = QSAPrefixDecode(cache, B, 1, Hq, 1, 1, 64, 200)
+    pos, L = ints(lens), ints([n + 1 for n in lens])
+    cu, cug, pl = ints([0, 1, 2, 3]), ints([0, 1]), ints([64])
+    qkv = queries((B, Hq + 2 * Hkv, D), "bf16", 62).cuda()
+    qr = torch.empty((B, Hq, D), dtype=torch.bfloat16, device="cuda")
+
+    def step(stream=None):
+        rope(pos, cu, qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], qr, stream=stream)
+        a = win(qr.view(B, 1, Hq, D), L, stream=stream)
+        b = pre(qr.view(B, 1, Hq, D), L, cug, pl, stream=stream)
+        return a, b
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        out = step()
+    for k in range(3):
+        qkv.copy_(queries((B, Hq + 2 * Hkv, D), "bf16", 70 + k))
+        pos += 1
+        L += 1
+        g.replay()
+        torch.cuda.synchronize()
+        c.k, c.v = cache.k_cache.cpu(), cache.v_cache.cpu()
+        now = [n + 2 + k for n in lens]
+        q = qr.cpu().view(B, 1, Hq, D)
+        want, _ = window_want(c, q, now, 1, 100, 4)
+        A.check(*out[0], want, "bf16", D, "window")
+        A.check(*out[1], prefix_want(c, q, now, 1), "bf16", D, "prefix")
+
+
+# ------------------------------------------------- recorded on the device --
+def test_bad_pages_lengths_and_offsets_are_recorded():
+    Hq, Hkv, D, page = 16, 2, 128, 64
+    c = A.PagedKV([100, 200], Hkv, D, "bf16", page, "cuda", seed=71)
+    q = queries((2, 1, Hq, D), "bf16", 72)
+    cache = c.cache()
+    dense = 2 ** 31 - 1
+    BOUNDS, BAD = 1, 4
+    # a length the block table cannot hold
+    QSAWindowDecode(cache, 2, 1, Hq, dense)(q.cuda(), ints([100, 100000]))
+    assert qsa_get_device_error()[1] & BOUNDS
+    # a page that is not there, and one beyond the pool: zeros in its place
+    for bad in (-1, 10 ** 6):
+        t = cache.block_table.clone()
+        cache.block_table[1, 1] = bad
+        o, lse = QSAWindowDecode(cache, 2, 1, Hq, dense)(q.cuda(), ints([100, 200]))
+        assert qsa_get_device_error()[1] & BOUNDS
+        K, V = (c.values(x, 1, range(200)) for x in "kv")
+        K[page:2 * page] = V[page:2 * page] = 0
+        want, _ = window_want(c, q, [100], 1, dense, 0)
+        A.check(o[:1], lse[:1], want, "bf16", D, "the other request")
+        part = A.stack([A.stack([A.attend(q[1, 0], K, V, D ** -0.5)])])
+        A.check(o[1:], lse[1:], part, "bf16", D, "without the page")
+        cache.block_table.copy_(t)
+    # offsets that fall, leave the rows, or break the bound
+    ch = QSAWindowPrefill(cache, 2, 8, 4, Hq, 64)
+    for cu in ([0, 5, 2], [0, 4, 9], [0, 5, 8], [-1, 2, 4]):
+        ch(q.view(2, Hq, D).repeat(4, 1, 1).cuda(), ints(cu), ints([100, 200]))
+        assert qsa_get_device_error()[1] & BAD
+    pr = QSAPrefixDecode(cache, 2, 1, Hq, 1, 1, 64, 200)
+    for cu, n in (([0, 2], 64), ([0, 3], 64), ([1, 0], 64), ([0, 1], -5)):
+        pr(q.cuda(), ints([100, 200]), ints(cu), ints([n]))
+        assert qsa_get_device_error()[1] & BAD
+    # a new token without a page: its query is still rotated
+    rope = QSARopeAppend(cache, Hq)
+    k = queries((2, Hkv, D), "bf16", 73).cuda()
+    before = cache.k_cache.clone()
+    out = rope(ints([10 ** 5, -1]), ints([0, 1, 2]), q.view(2, Hq, D).cuda(), k, k)
+    assert qsa_get_device_error()[1] & BOUNDS
+    assert torch.equal(before, cache.k_cache)
+    y, mag = A.rope_row(q[0, 0], 10 ** 5, rope.inv_freq, 1.0, D, False)
+    assert ((out[0].double().cpu() - y).abs() <= 2.0 ** -8 * y.abs() + 2.0 ** -19 * mag).all()
