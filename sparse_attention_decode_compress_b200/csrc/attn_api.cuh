@@ -6,6 +6,7 @@
 #include "attn_common.cuh"
 #include "attn_decode.cuh"
 #include "attn_simple.cuh"
+#include "attn_tile.cuh"
 #include "rope_append.cuh"
 
 namespace {
@@ -43,6 +44,16 @@ AttnPlan plan_stream(long long seqs, int Hkv, long long span) {
   p.tiles = 1;
   const long long pairs = std::max(1LL, seqs * Hkv);
   p.splits = (int)std::max(1LL, std::min({4LL * kPlanSMs / pairs, ceil_ll(span, 256), 64LL}));
+  return p;
+}
+
+// Many rows of a 16-bit or 8-bit cache: one CTA (an SM's) of the tensor-core
+// kernel per (sequence, kv head, 256 rows, split).
+AttnPlan plan_tiles(long long seqs, int Hkv, long long rows, long long span) {
+  AttnPlan p;
+  p.tiles = ceil_ll(std::max(rows, 1LL), 2 * qsa::attn::kTileRows);
+  const long long ctas = std::max(1LL, seqs * Hkv * p.tiles);
+  p.splits = (int)std::max(1LL, std::min({kPlanSMs / ctas, ceil_ll(span, 4 * qsa::attn::kTileKeys), 64LL}));
   return p;
 }
 
@@ -102,20 +113,24 @@ void set_parts(qsa::attn::Args &a, int slots, void *workspace) {
 }
 
 // ----------------------------------------------------------------- launch --
-template <int MODE, int D, typename QT, typename KT>
+template <int MODE, int D>
 qsa_status launch_simple(const qsa::attn::Args &a, const AttnPlan &pl, long long seqs, cudaStream_t s) {
   const dim3 grid((unsigned)pl.tiles, (unsigned)(a.c.num_kv_heads * pl.splits), (unsigned)seqs);
-  return launch(true, qsa::attn::simple_kernel<MODE, D, QT, KT>, grid, dim3(qsa::attn::kSimpleThreads),
+  return launch(true, qsa::attn::simple_kernel<MODE, D>, grid, dim3(qsa::attn::kSimpleThreads),
                 sizeof(qsa::attn::SimpleSmem<D>), s, a);
 }
 
-template <int MODE, int D>
-qsa_status launch_simple_d(const qsa::attn::Args &a, const AttnPlan &pl, long long seqs, cudaStream_t s) {
-  switch (a.c.kv_dtype) {
-    case QSA_F32: return launch_simple<MODE, D, float, float>(a, pl, seqs, s);
-    case QSA_BF16: return launch_simple<MODE, D, __nv_bfloat16, __nv_bfloat16>(a, pl, seqs, s);
-    default: return launch_simple<MODE, D, __nv_bfloat16, __nv_fp8_e4m3>(a, pl, seqs, s);
+template <int MODE, int D, bool FP8>
+qsa_status launch_tile(const qsa::attn::Args &a, const AttnPlan &pl, long long seqs, cudaStream_t s) {
+  static bool done[kMaxDevices] = {false};
+  auto kernel = qsa::attn::tile_kernel<MODE, D, FP8>;
+  const size_t smem = sizeof(qsa::attn::TileSmem<D>) + 1024;
+  {
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if (prepare_kernel(kernel, smem, done) != cudaSuccess) return QSA_ERR_CUDA;
   }
+  return launch(true, kernel, dim3((unsigned)pl.tiles, (unsigned)(a.c.num_kv_heads * pl.splits), (unsigned)seqs),
+                dim3(qsa::attn::kTileThreads), smem, s, a);
 }
 
 // The rows of `seqs` sequences, as pl splits them.
@@ -125,7 +140,15 @@ qsa_status launch_rows(qsa::attn::Args a, const AttnPlan &pl, long long seqs, in
   a.splits = pl.splits;
   if (pl.tiles > 0x7fffffffLL || (long long)a.c.num_kv_heads * pl.splits > 65535 || seqs > 65535)
     return QSA_ERR_UNSUPPORTED;
-  return a.c.head_dim == 64 ? launch_simple_d<MODE, 64>(a, pl, seqs, s) : launch_simple_d<MODE, 128>(a, pl, seqs, s);
+  if (a.c.kv_dtype == QSA_F32)
+    return a.c.head_dim == 64 ? launch_simple<MODE, 64>(a, pl, seqs, s) : launch_simple<MODE, 128>(a, pl, seqs, s);
+  if constexpr (MODE != qsa::attn::kTail) {
+    const bool fp8 = a.c.kv_dtype == QSA_FP8_E4M3;
+    if (a.c.head_dim == 64)
+      return fp8 ? launch_tile<MODE, 64, true>(a, pl, seqs, s) : launch_tile<MODE, 64, false>(a, pl, seqs, s);
+    return fp8 ? launch_tile<MODE, 128, true>(a, pl, seqs, s) : launch_tile<MODE, 128, false>(a, pl, seqs, s);
+  }
+  return QSA_ERR_UNSUPPORTED;  // (a 16-bit cache's tails are decode rows)
 }
 
 template <int MODE, int D, bool FP8, int NT>
@@ -181,10 +204,13 @@ AttnPlan plan_decode(const qsa_cache *c, int B, int T, int Hq, long long window,
 
 AttnPlan plan_chunk(const qsa_cache *c, int B, long long max_q, int Hq, long long window, long long sinks) {
   const long long span = span_bound(window, sinks, max_q, ctx_cap(c));
+  if (c->kv_dtype != QSA_F32) return plan_tiles(B, c->num_kv_heads, max_q * (Hq / c->num_kv_heads), span);
   return plan_simple(B, c->num_kv_heads, max_q * (Hq / c->num_kv_heads), span);
 }
 
 AttnPlan plan_shared(const qsa_cache *c, int n_groups, long long max_group, int T, int Hq, long long max_prefix) {
+  if (c->kv_dtype != QSA_F32)
+    return plan_tiles(n_groups, c->num_kv_heads, max_group * T * (Hq / c->num_kv_heads), max_prefix);
   return plan_simple(n_groups, c->num_kv_heads, max_group * T * (Hq / c->num_kv_heads), max_prefix);
 }
 

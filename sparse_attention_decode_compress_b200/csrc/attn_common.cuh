@@ -227,9 +227,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(Args a) {
   const int S = a.slots;
   const float *lp = a.lse_part + row * S;
   float mx = -INFINITY;
-  for (int k = lane; k < S; k += 32) mx = fmaxf(mx, __ldcg(lp + k));
+  bool nan = false;
+  for (int k = lane; k < S; k += 32) {
+    const float l = __ldcg(lp + k);
+    nan |= l != l;
+    mx = fmaxf(mx, l);
+  }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  if (__any_sync(0xffffffffu, nan)) mx = NAN;  // a NaN in any part is one in the result
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f;
   const int d = 4 * lane;
@@ -248,13 +254,13 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(Args a) {
       }
     }
   }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const float inv = z != 0.f ? 1.f / z : 0.f;
   acc.x *= inv;
   acc.y *= inv;
   acc.z *= inv;
   acc.w *= inv;
   if (d < D) store4(static_cast<OutT *>(a.o) + row * D + d, acc);
-  if (lane == 0) a.lse[row] = z > 0.f ? mx + __logf(z) : -INFINITY;
+  if (lane == 0) a.lse[row] = z != 0.f ? mx + __logf(z) : -INFINITY;
 }
 
 }  // namespace attn

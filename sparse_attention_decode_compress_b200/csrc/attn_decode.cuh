@@ -356,30 +356,29 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, sm.m[w][m]);
+    if (mx == -INFINITY) mx = 0.f;
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mx != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float f = attn::ex2(sm.m[w][m] - mx);
-        const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][m][d]);
-        l += f * sm.l[w][m];
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
-      }
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float f = attn::ex2(sm.m[w][m] - mx);
+      const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][m][d]);
+      l += f * sm.l[w][m];
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN sum stays one)
     acc.x *= inv;
     acc.y *= inv;
     acc.z *= inv;
     acc.w *= inv;
     const long long at = (long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G;
-    const float lse = l > 0.f ? (mx + __log2f(l)) * attn::kLn2 : -INFINITY;
+    const float lse = l != 0.f ? (mx + __log2f(l)) * attn::kLn2 : -INFINITY;
     if (a.slots > 1) {
       const long long slot = at * a.slots + a.slot0 + split;
-      if (l > 0.f) store4(a.o_part + slot * D + d, acc);
+      if (l != 0.f) store4(a.o_part + slot * D + d, acc);
       if (d == 0) {
         a.lse_part[slot] = lse;
         if (MODE == kTail && split == 0 && !sq.grouped)

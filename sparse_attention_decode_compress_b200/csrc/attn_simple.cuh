@@ -23,19 +23,12 @@ struct SimpleSmem {
   float v[kSimpleKeys][D];
 };
 
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-  const uint2 w = *reinterpret_cast<const uint2 *>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
-__device__ __forceinline__ float4 load4(const __nv_fp8_e4m3 *p) {
-  const __nv_fp8x4_e4m3 w = *reinterpret_cast<const __nv_fp8x4_e4m3 *>(p);
-  return static_cast<float4>(w);
+__device__ __forceinline__ float4 load4(const void *p, long long at) {
+  return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
 }
 
 // Grid (row tiles, Hkv * splits, sequences).
-template <int MODE, int D, typename QT, typename KT>
+template <int MODE, int D>
 __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
   pdl_open();
   constexpr int kVec = D / 4;
@@ -59,7 +52,7 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
     if (m < rows) {
       const int row = m0 + m;
       const long long at = ((long long)(sq.tok0 + row / a.G) * a.Hq + g * a.G + row % a.G) * D;
-      v = load4(static_cast<const QT *>(a.q) + at + d);
+      v = load4(a.q, at + d);
     }
     *reinterpret_cast<float4 *>(&sm.q[m][d]) = v;
   }
@@ -88,14 +81,8 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
         if (pg >= 0) {
           const long long at =
               (((long long)pg * a.c.page_size + (key - lp * a.c.page_size)) * a.c.num_kv_heads + g) * D + d;
-          kv = load4(static_cast<const KT *>(a.c.k_cache) + at);
-          vv = load4(static_cast<const KT *>(a.c.v_cache) + at);
-          if (a.c.k_scale) {
-            const float ks = a.c.k_scale[(long long)pg * a.c.num_kv_heads + g];
-            const float vs = a.c.v_scale[(long long)pg * a.c.num_kv_heads + g];
-            kv.x *= ks, kv.y *= ks, kv.z *= ks, kv.w *= ks;
-            vv.x *= vs, vv.y *= vs, vv.z *= vs, vv.w *= vs;
-          }
+          kv = load4(a.c.k_cache, at);
+          vv = load4(a.c.v_cache, at);
         }
       }
       *reinterpret_cast<float4 *>(&sm.k[j][d]) = kv;
@@ -153,8 +140,9 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
     float t = l[j];
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    const float inv = t > 0.f ? 1.f / t : 0.f;
-    const float lse = t > 0.f ? (mx[j] + __log2f(t)) * kLn2 : -INFINITY;
+    // (a NaN sum stays one)
+    const float inv = t != 0.f ? 1.f / t : 0.f;
+    const float lse = t != 0.f ? ((mx[j] == -INFINITY ? 0.f : mx[j]) + __log2f(t)) * kLn2 : -INFINITY;
     const int row = m0 + m;
     const long long at = (long long)(sq.tok0 + row / a.G) * a.Hq + g * a.G + row % a.G;
     if (a.slots > 1) {
@@ -163,7 +151,7 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
       // a request outside every group: nothing else writes its shared slots
       if (MODE == kTail && split == 0 && !sq.grouped)
         for (int k = lane; k < a.slot0; k += 32) a.lse_part[at * a.slots + k] = -INFINITY;
-      if (t > 0.f) {
+      if (t != 0.f) {
 #pragma unroll
         for (int i = 0; i < kDims; ++i) a.o_part[slot * D + lane + 32 * i] = o[j][i] * inv;
       }
@@ -171,7 +159,7 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
       if (lane == 0) a.lse[at] = lse;
 #pragma unroll
       for (int i = 0; i < kDims; ++i)
-        static_cast<QT *>(a.o)[at * D + lane + 32 * i] = static_cast<QT>(o[j][i] * inv);
+        static_cast<float *>(a.o)[at * D + lane + 32 * i] = o[j][i] * inv;
     }
   }
 }
