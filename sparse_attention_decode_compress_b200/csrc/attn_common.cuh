@@ -168,7 +168,7 @@ __device__ __forceinline__ Range range_of(const Args &a, const Seq &q, int i0, i
   }
   if (hi <= 0) return r;
   // a length that the block table cannot hold is cut to what it can
-  const long long cap = (long long)a.c.max_pages_per_req * a.c.page_size;
+  const long long cap = min((long long)a.c.max_pages_per_req * a.c.page_size, 0x7fffff00LL);
   if (hi > cap) {
     record_error(kErrBounds);
     hi = (int)cap;

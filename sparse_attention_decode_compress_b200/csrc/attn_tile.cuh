@@ -11,22 +11,25 @@
 //     tile run, the tensor core works on the other.
 //   - warps 0-3, 4-7   softmax of tile 0 / 1, a thread per row: scores from
 //     tensor memory, running maximum and sum in registers, weights back to
-//     tensor memory as bf16, where the value product reads them as its A
+//     tensor memory in 16 bits, where the value product reads them as its A
 //     operand (they take the place of the scores)
-//   - warp 8           one thread issues every product: values of a tile, then
-//     the scores of its next keys
-//   - warps 9-12       fill the ring of key and value tiles: rows are gathered
+//   - warps 8-11       fill the ring of key and value tiles: rows are gathered
 //     page by page with 16-byte cp.async (any page size), fp8 rows are
-//     converted on the way
+//     converted to f16 on the way
+//   - warp 12          one thread issues every product: values of a tile, then
+//     the scores of its next keys (warps 13-15 only complete the warpgroup that
+//     gives its registers to the softmax)
 // The output accumulators stay in tensor memory.  They are rescaled only when
 // a row's maximum has grown by more than 2^8 since the last time (weights up to
 // 2^8 lose nothing in bf16 and float32), by the thread that owns the row: the
 // scores of step j are issued behind the values of step j - 1, so that thread
 // has them to itself between the two.
 //
-// Rounding: weights to bf16 (2^-9 relative), the error of the output's own
-// rounding; fp8 keys are exact in bf16 and their scale multiplies the score in
-// float32; fp8 values times their scale are rounded to bf16.
+// Rounding: weights to bf16, the error of the output's own rounding.  fp8
+// caches run in f16, which holds every E4M3 code: queries scaled per row by a
+// power of two (fp8_frag.cuh says what that keeps), the key scale on the score
+// in float32, and the value scale, relative to a power of two that follows the
+// largest one seen, on the weight before it is rounded to f16 (2^-12).
 #pragma once
 #include "attn_common.cuh"
 #include "fp8_frag.cuh"
@@ -39,7 +42,8 @@ constexpr int kTileRows = 128;  // rows of one tile (MMA M)
 constexpr int kTileKeys = 128;
 constexpr int kTileSlots = 4;   // ring: key and value tiles in turn
 constexpr int kTileLoaders = 4;  // warps
-constexpr int kTileThreads = (8 + 1 + kTileLoaders) * 32;
+constexpr int kTileThreads = 16 * 32;
+constexpr int kLoadWarp = 8, kMmaWarp = 12;
 constexpr uint32_t kTmemCols = 512;  // S0, S1 at 0 and 128, O0, O1 at 256 and 384
 constexpr float kLazy = 8.f;    // growth of a row's maximum (log2) that is left in the weights
 constexpr unsigned long long kTileWaitNs = 2000000000ull;
@@ -49,7 +53,9 @@ struct TileSmem {
   static constexpr int kTile = kTileKeys * D * 2;  // bytes of a key, value or query tile
   uint8_t q[2][kTile];
   uint8_t ring[kTileSlots][kTile];
-  float kscale[4][kTileKeys];  // fp8: key scale * sm_scale * log2(e), by key tile
+  // fp8: scales of a tile's keys and values, the largest |value scale| of each
+  // loader's share, and 2^-e of each query row (the row is scaled by 2^e)
+  float kscale[4][kTileKeys], vscale[4][kTileKeys], vmax[4][kTileLoaders], qscale[2 * kTileRows];
   alignas(8) uint64_t full[kTileSlots], empty[kTileSlots];
   uint64_t qfull, sfull[2], pfull[2], ofull[2];
   uint32_t tmem;
@@ -61,6 +67,10 @@ __device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t n) {
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+// Arrives when this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void mbar_arrive_copies(uint64_t *b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
   uint32_t ok;
@@ -135,10 +145,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) 
 #undef QSA_W8
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// kind::f16 with bf16 operands and a float32 accumulator, M = 128; B read
-// K-major (keys) or MN-major (values).
-__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+// kind::f16 with bf16 or f16 operands and a float32 accumulator, M = 128; B
+// read K-major (keys) or MN-major (values).
+__host__ __device__ constexpr uint32_t idesc_16(bool bf16, int n, bool b_mn) {
+  return (1u << 4) | (bf16 ? 1u << 7 | 1u << 10 : 0u) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kTileRows >> 4) << 24);
 }
 // A tile is D / 64 column blocks of 128 rows x 128 bytes, 128-byte swizzled.
@@ -154,11 +164,154 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t at) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Two f16 pairs (from E4M3) times a scale to bf16 pairs.
-__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float s) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-  const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-  return *reinterpret_cast<const uint32_t *>(&b);
+// Two float32 in a register pair.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float x, float y) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&b);
+  } else {
+    return dec::pack_f16(x, y);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A row's weights of one step: the scores in tensor memory become weights
+// relative to the (possibly raised) maximum mx, the sum l and, when the
+// reference moves, the output accumulators follow.  see(c): the keys c .. c + 31
+// of the tile that the row sees, as bits (MASKED).
+template <int D, bool FP8, bool MASKED, typename See>
+__device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first, float scale, const float *ksc,
+                                        const float *vsc, const float *vmax, float &vref, float &mx, float &l,
+                                        See see) {
+  uint32_t s[4][32];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) tmem_ld32(s_at + 32 * q, s[q]);
+  pre::tmem_ld_wait();
+  float tops[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t bits = MASKED ? see(32 * q) : 0u;
+    if (FP8) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 k = *reinterpret_cast<const float4 *>(ksc + 32 * q + e);
+        s[q][e] = __float_as_uint(__uint_as_float(s[q][e]) * k.x);
+        s[q][e + 1] = __float_as_uint(__uint_as_float(s[q][e + 1]) * k.y);
+        s[q][e + 2] = __float_as_uint(__uint_as_float(s[q][e + 2]) * k.z);
+        s[q][e + 3] = __float_as_uint(__uint_as_float(s[q][e + 3]) * k.w);
+      }
+    }
+    if (MASKED) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!((bits >> e) & 1u)) s[q][e] = 0xff800000u;  // -inf
+    }
+    float t = __uint_as_float(s[q][0]);
+#pragma unroll
+    for (int e = 1; e < 31; e += 2) t = max3(t, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+    tops[q] = fmaxf(t, __uint_as_float(s[q][31]));
+  }
+  const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
+  const bool grow = top > mx + kLazy || (mx == -INFINITY && top > -INFINITY);
+  const float m_new = grow ? top : mx;
+  float al = grow ? (mx == -INFINITY ? 0.f : ex2(mx - m_new)) : 1.f;
+  l *= al;
+  bool move = grow;
+  if (FP8) {
+    const float4 w = *reinterpret_cast<const float4 *>(vmax);
+    const float v = fmaxf(max3(w.x, w.y, w.z), w.w);
+    const float ref = dec::vs_binade(v);
+    if (v > 0.f && ref > vref) {
+      al *= vref / ref;
+      vref = ref;
+      move = true;
+    }
+  }
+  if (__any_sync(0xffffffffu, move) && !first) {
+#pragma unroll
+    for (int c = 0; c < D; c += 16) {
+      uint32_t v[16];
+      pre::tmem_ld16(o_at + c, v);
+      pre::tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+      tmem_st16(o_at + c, v);
+    }
+  }
+  mx = m_new;
+  const float base = mx == -INFINITY ? 0.f : mx;
+  const f2 sc2 = pack2(scale, scale), nb2 = pack2(-base, -base);
+  const float vinv = FP8 && vref > 0.f ? 1.f / vref : 0.f;
+  f2 sum0 = 0, sum1 = 0;  // (0.f, 0.f)
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t p[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      float x0, x1, x2, x3;
+      unpack2(fma2(pack2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), sc2, nb2), x0, x1);
+      unpack2(fma2(pack2(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), sc2, nb2), x2, x3);
+      x0 = ex2(x0);
+      x1 = ex2(x1);
+      x2 = ex2(x2);
+      x3 = ex2(x3);
+      sum0 = add2(sum0, pack2(x0, x1));
+      sum1 = add2(sum1, pack2(x2, x3));
+      if (FP8) {
+        const float4 v = *reinterpret_cast<const float4 *>(vsc + 32 * q + e);
+        x0 *= v.x * vinv;
+        x1 *= v.y * vinv;
+        x2 *= v.z * vinv;
+        x3 *= v.w * vinv;
+      }
+      p[e / 2] = pack16<!FP8>(x0, x1);
+      p[e / 2 + 1] = pack16<!FP8>(x2, x3);
+    }
+    tmem_st16(s_at + 16 * q, p);
+  }
+  float a, b, c, d;
+  unpack2(sum0, a, b);
+  unpack2(sum1, c, d);
+  l += (a + b) + (c + d);
+  tmem_st_wait();
 }
 
 // Grid (row tiles of 256, Hkv * splits, sequences).
@@ -182,18 +335,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
   const int nt = (x1 - x0 + kTileKeys - 1) / kTileKeys;
   const int tiles = rows > kTileRows ? 2 : 1;
 
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)),
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
+    // bf16: every loader thread's copies; fp8: every loader warp
+    constexpr uint32_t kArrivals = FP8 ? kTileLoaders : kTileLoaders * 32;
     for (int i = 0; i < kTileSlots; ++i) {
-      mbar_init(&sm.full[i], kTileLoaders);
+      mbar_init(&sm.full[i], kArrivals);
       mbar_init(&sm.empty[i], 1);
     }
-    mbar_init(&sm.qfull, kTileLoaders);
+    mbar_init(&sm.qfull, kArrivals);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.sfull[t], 1);
       mbar_init(&sm.pfull[t], 4);
@@ -207,8 +362,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
   pre::tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  if (warp < 8) {
+  // registers: 512 threads start with 128 each; the shares add up to that
+  constexpr int kRegsSoftmax = FP8 ? 176 : 192, kRegsLoad = FP8 ? 104 : 72, kRegsMma = 56;
+  static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsMma <= 4 * 128, "register shares");
+  if (warp < kLoadWarp) {
     // ------------------------------------------------------------ softmax --
+    regs_up<kRegsSoftmax>();
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int m = m0 + t * kTileRows + row;
@@ -225,82 +384,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
       vc = min(rg.sa + v.hi - rg.b0, rg.n);
     }
     float mx = -INFINITY, l = 0.f;  // maximum (scaled, log2) the weights are relative to, and their sum
+    float vref = 0.f;  // fp8: power of two that the value scales are relative to
     bool ok = true;
     if (t < tiles) {
-      for (int j = 0; j < nt; ++j) {
+      float scale = a.scale_log2;
+      if (FP8) {
+        ok = __all_sync(0xffffffffu, mbar_wait_or(&sm.qfull, 0, &sm.dead));
+        scale *= sm.qscale[t * kTileRows + row];
+      }
+      for (int j = 0; ok && j < nt; ++j) {
         const int xt = x0 + j * kTileKeys;
         ok = mbar_wait_or(&sm.sfull[t], j & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         pre::tc_fence_after();
         const bool whole = !live || (xt >= vb && xt + kTileKeys <= vc) || xt + kTileKeys <= va;
         const bool masked = !__all_sync(0xffffffffu, whole);
-        const float *ksc = FP8 ? sm.kscale[j & 3] : nullptr;
-        auto bits = [&](int c) -> uint32_t {  // keys xt + c .. + 31 that the row sees
+        auto see = [&](int c) -> uint32_t {  // keys xt + c .. + 31 that the row sees
           const int x = xt + c;
           auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
           return below(va - x) | (below(vc - x) & ~below(vb - x));
         };
-        // ---- the row's maximum
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kTileKeys; c += 32) {
-          uint32_t s[32];
-          tmem_ld32(s_at + c, s);
-          pre::tmem_ld_wait();
-          const uint32_t see = masked ? bits(c) : 0xffffffffu;
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float y = __uint_as_float(s[e]);
-            if (FP8) y *= ksc[c + e];
-            if (masked && !((see >> e) & 1u)) y = -INFINITY;
-            top = fmaxf(top, y);
-          }
-        }
-        if (!FP8) top *= a.scale_log2;
-        const bool grow = top > mx + kLazy || (mx == -INFINITY && top > -INFINITY);
-        const float m_new = grow ? top : mx;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float al = grow ? (mx == -INFINITY ? 0.f : ex2(mx - m_new)) : 1.f;
-          l *= al;
-          if (j > 0) {
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t v[32];
-              tmem_ld32(o_at + c, v);
-              pre::tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-              tmem_st32(o_at + c, v);
-            }
-          }
-        }
-        mx = m_new;
-        const float base = mx == -INFINITY ? 0.f : mx;
-        // ---- weights, as bf16 in the place of the scores
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < kTileKeys; c += 32) {
-          uint32_t s[32], p[16];
-          tmem_ld32(s_at + c, s);
-          pre::tmem_ld_wait();
-          const uint32_t see = masked ? bits(c) : 0xffffffffu;
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(s[e]), FP8 ? ksc[c + e] : a.scale_log2, -base));
-            float p1 = ex2(fmaf(__uint_as_float(s[e + 1]), FP8 ? ksc[c + e + 1] : a.scale_log2, -base));
-            if (masked) {
-              if (!((see >> e) & 1u)) p0 = 0.f;
-              if (!((see >> (e + 1)) & 1u)) p1 = 0.f;
-            }
-            l0 += p0;
-            l1 += p1;
-            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-            p[e / 2] = *reinterpret_cast<const uint32_t *>(&b);
-          }
-          tmem_st16(s_at + c / 2, p);
-        }
-        l += l0 + l1;
-        tmem_st_wait();
+        if (masked)
+          weights<D, FP8, true>(s_at, o_at, j == 0, scale, sm.kscale[j & 3], sm.vscale[j & 3], sm.vmax[j & 3], vref,
+                                mx, l, see);
+        else
+          weights<D, FP8, false>(s_at, o_at, j == 0, scale, sm.kscale[j & 3], sm.vscale[j & 3], sm.vmax[j & 3], vref,
+                                 mx, l, see);
         pre::tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pfull[t]);
@@ -310,7 +419,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
       ok = __all_sync(0xffffffffu, ok);
       pre::tc_fence_after();
       const bool some = l != 0.f;  // (a NaN sum stays one)
-      const float inv = some ? 1.f / l : 0.f;
+      const float inv = some ? (FP8 ? vref / l : 1.f / l) : 0.f;
       const float lse = some ? ((mx == -INFINITY ? 0.f : mx) + __log2f(l)) * kLn2 : -INFINITY;
       const long long at = (long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G;
       const long long slot = at * a.slots + a.slot0 + split;
@@ -348,10 +457,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ products --
-    if (lane == 0 && nt > 0) {
-      const uint32_t idesc_s = idesc_bf16(kTileKeys, false), idesc_o = idesc_bf16(D, true);
+    regs_down<kRegsMma>();
+    if (warp == kMmaWarp && lane == 0 && nt > 0) {
+      const uint32_t idesc_s = idesc_16(!FP8, kTileKeys, false), idesc_o = idesc_16(!FP8, D, true);
       auto scores = [&](int t, int slot) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -362,6 +472,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
       };
       bool ok = mbar_wait_or(&sm.qfull, 0, &sm.dead) && mbar_wait_or(&sm.full[0], 0, &sm.dead);
       if (ok) {
+        // what the loaders wrote goes over to the tensor core's view here, where
+        // it is waited for: in the loaders the fence would wait for the copies
+        // still in flight
+        pre::fence_async_smem();
         pre::tc_fence_after();
         for (int t = 0; t < tiles; ++t) {
           scores(t, 0);
@@ -374,6 +488,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
         const bool more = j + 1 < nt;
         ok = mbar_wait_or(&sm.full[nv % kTileSlots], (nv / kTileSlots) & 1, &sm.dead);
         if (ok && more) ok = mbar_wait_or(&sm.full[nk % kTileSlots], (nk / kTileSlots) & 1, &sm.dead);
+        pre::fence_async_smem();
         for (int t = 0; ok && t < tiles; ++t) {
           ok = mbar_wait_or(&sm.pfull[t], j & 1, &sm.dead);
           if (!ok) break;
@@ -395,9 +510,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
       }
     }
     __syncwarp();
-  } else if (nt > 0) {
+  } else {
     // -------------------------------------------------------------- loaders --
-    const int wl = warp - 9;
+    regs_down<kRegsLoad>();
+    const int wl = warp - kLoadWarp;
     constexpr int kRowBytes = D * (FP8 ? 1 : 2);
     constexpr int kChunks = kRowBytes / 16;
     constexpr int kRowsPer = 32 / kChunks;          // rows of one load of the warp
@@ -416,7 +532,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
         const bool ok = rr < rows;
         const __nv_bfloat16 *src =
             ok ? qg + ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D + ch * 8 : qg;
-        cp_async16_zfill(sm.q[rr / kTileRows] + tile_off(rr % kTileRows, ch), src, ok);
+        uint8_t *dst = sm.q[rr / kTileRows] + tile_off(rr % kTileRows, ch);
+        if constexpr (!FP8) {
+          cp_async16_zfill(dst, src, ok);
+        } else {
+          // f16, scaled so that 2^14 <= max |q| 2^e < 2^15; kQ lanes hold a row
+          const uint4 x = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t mxq = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mxq = max(mxq, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int off = kQ / 2; off >= 1; off >>= 1) mxq = max(mxq, __shfl_xor_sync(0xffffffffu, mxq, off));
+          const int ex = mxq == 0u ? 0 : min(141 - (int)(mxq >> 7), 126);
+          const float f = dec::pow2f(ex);
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = dec::pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+          if (ch == 0) sm.qscale[rr] = dec::pow2f(-ex);
+        }
       }
       cp_async_commit();
     }
@@ -424,50 +560,85 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
     Seen any = seen_by<MODE>(a, sq, i1 - 1);
     if (MODE == kWindow) any.lo = max(0, sq.first + i0 + 1 - a.window);
     if (MODE == kShared) any.hi = sq.prefix;
-    // lane i < 8: token row of this warp's keys 4 i .. 4 i + 3 of a tile
-    auto lookup = [&](int j, long long &row, float &ks, float &vs) {
-      row = -1;
-      ks = vs = 0.f;
+    // lane i < 8: the block-table entry of this warp's keys 4 i .. 4 i + 3 of a
+    // tile, loaded a step ahead of its use (-1: none is needed)
+    const long long table = (long long)sq.table * a.c.max_pages_per_req;
+    auto lookup = [&](int j, int &pg, int &in_page) {
+      pg = -1;
+      in_page = 0;
       const int x = x0 + j * kTileKeys + wl * kRowsWarp + 4 * lane;
       if (lane < kRowsWarp / 4 && x < x1) {
-        const int key = rg.key(x);
+        const int key = rg.key(x);  // below max_pages_per_req * page_size (range_of)
         const int lp = key / a.c.page_size;
-        const int pg = physical_page(a.c, sq.table, lp);
-        if (pg >= 0) {
-          row = (long long)pg * a.c.page_size + (key - lp * a.c.page_size);
+        in_page = key - lp * a.c.page_size;
+        pg = a.c.block_table[table + lp];
+        if (pg < 0) pg = -2;
+      }
+    };
+    // A tile's rows as the lanes load them: load i covers rows kRowsPer i .. of
+    // the warp's 32, lane / kChunks picking the row and lane % kChunks its 16
+    // bytes.  Four rows share an offset, found once for the keys and the values.
+    constexpr int kOffs = kRowsPer == 2 ? kLoads / 2 : kLoads;
+    const int lr = lane / kChunks, ch = lane % kChunks;
+    const long long in_group = (lr & 3) * row_stride + ch * 16, two_rows = 2 * row_stride;
+    long long off[kOffs];
+    bool whole = false;  // every row of the warp's share is loaded
+    int xw = 0;          // virtual key of its first row
+    float ks = 0.f, vs = 0.f;  // fp8: scales of the keys' page
+    auto place = [&](int j, int pg, int in_page) {
+      long long row = -1;
+      ks = vs = 0.f;
+      if (pg != -1) {
+        if (pg < 0 || pg >= a.c.num_pages) {
+          record_error(kErrBounds);
+        } else {
+          row = ((long long)pg * a.c.page_size + in_page) * row_stride;
           if (FP8) {
             ks = a.c.k_scale[(long long)pg * Hkv + g];
             vs = a.c.v_scale[(long long)pg * Hkv + g];
           }
         }
       }
+      xw = x0 + j * kTileKeys + wl * kRowsWarp;
+      const int k0 = rg.key(xw), k1 = rg.key(xw + kRowsWarp - 1);
+      whole = __all_sync(0xffffffffu, lane >= kRowsWarp / 4 || row >= 0) && xw + kRowsWarp <= x1 &&
+              k1 - k0 == kRowsWarp - 1 && k1 < any.hi && (k0 >= any.lo || k1 < any.sink);
+#pragma unroll
+      for (int k = 0; k < kOffs; ++k) {
+        const int at = kRowsPer == 2 ? k : kRowsPer == 4 ? k : 2 * k + (lr >> 2);
+        off[k] = __shfl_sync(0xffffffffu, row, at) + in_group;
+      }
+      if (!whole) {
+        // the rows that nothing sees, or without a page, are marked
+#pragma unroll
+        for (int k = 0; k < kOffs; ++k) {
+          const int at = kRowsPer == 2 ? k : kRowsPer == 4 ? k : 2 * k + (lr >> 2);
+          if (__shfl_sync(0xffffffffu, row, at) < 0) off[k] = -1;
+        }
+      }
     };
-    // source of load i of tile j (nullptr: zeros)
-    auto source = [&](int j, int i, int kv, long long row, int &r) -> const uint8_t * {
-      r = i * kRowsPer + lane / kChunks;  // within the warp's 32 rows
-      const int ch = lane % kChunks;
-      const long long r0 = __shfl_sync(0xffffffffu, row, r >> 2);
-      const int x = x0 + j * kTileKeys + wl * kRowsWarp + r;
-      const bool ok = x < x1 && r0 >= 0 && sees(any, rg.key(x));
-      return ok ? base[kv] + (r0 + (r & 3)) * row_stride + ch * 16 : nullptr;
+    auto source = [&](int i, int kv, bool &ok) -> const uint8_t * {
+      const long long o = kRowsPer == 2 ? off[i / 2] + (i & 1) * two_rows : off[i];
+      ok = true;
+      if (!whole) {
+        const int x = xw + i * kRowsPer + lr;
+        ok = x < x1 && (kRowsPer == 2 ? off[i / 2] : off[i]) >= 0 && sees(any, rg.key(x));
+      }
+      return ok ? base[kv] + o : base[kv];
     };
-    long long row_cur, row_next;
-    float ks_cur, vs_cur, ks_next, vs_next;
-    lookup(0, row_cur, ks_cur, vs_cur);
-    lookup(1, row_next, ks_next, vs_next);
+    int pg_next, in_next;
+    lookup(0, pg_next, in_next);
+    place(0, pg_next, in_next);
+    lookup(1, pg_next, in_next);
     bool ok = true;
     if constexpr (!FP8) {
       // tile n of the ring: keys (n even) or values (n odd) of step n / 2
-      auto publish = [&](uint64_t *bar) {
-        pre::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
+      mbar_arrive_copies(&sm.qfull);
       for (int n = 0; n < 2 * nt; ++n) {
         const int j = n >> 1, slot = n % kTileSlots;
         if (n >= 2 && (n & 1) == 0) {
-          row_cur = row_next;
-          lookup(j + 1, row_next, ks_next, vs_next);
+          place(j, pg_next, in_next);
+          lookup(j + 1, pg_next, in_next);
         }
         if (n >= kTileSlots) {
           ok = mbar_wait_or(&sm.empty[slot], ((n / kTileSlots) - 1) & 1, &sm.dead);
@@ -475,48 +646,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
         }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          int r;
-          const uint8_t *src = source(j, i, n & 1, row_cur, r);
-          cp_async16_zfill(sm.ring[slot] + tile_off(wl * kRowsWarp + r, lane % kChunks), src ? src : base[0],
-                           src != nullptr);
+          bool ld;
+          const uint8_t *src = source(i, n & 1, ld);
+          cp_async16_zfill(sm.ring[slot] + tile_off(wl * kRowsWarp + i * kRowsPer + lr, ch), src, ld);
         }
-        cp_async_commit();
-        // two tiles stay in flight
-        cp_async_wait<2>();
-        if (n == 1) publish(&sm.qfull);
-        if (n >= 2) publish(&sm.full[(n - 2) % kTileSlots]);
+        mbar_arrive_copies(&sm.full[slot]);
       }
+      cp_async_commit();
       cp_async_wait<0>();
-      for (int n = max(0, 2 * nt - 2); n < 2 * nt; ++n) publish(&sm.full[n % kTileSlots]);
     } else {
       // fp8: raw rows of the next tile are loaded while this one is converted
       uint4 raw[2][kLoads];
-      auto fetch = [&](int n, uint4(&v)[kLoads], long long row) {
+      auto fetch = [&](int kv, uint4(&v)[kLoads]) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          int r;
-          const uint8_t *src = source(n >> 1, i, n & 1, row, r);
-          v[i] = src ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+          bool ld;
+          const uint8_t *src = source(i, kv, ld);
+          v[i] = ld ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
         }
       };
-      fetch(0, raw[0], row_cur);
-      cp_async_wait<0>();
-      pre::fence_async_smem();
+      if (nt > 0) fetch(0, raw[0]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.qfull);
       for (int j = 0; j < nt && ok; ++j) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const int n = 2 * j + kv, slot = n % kTileSlots;
-          const float vs_now = vs_cur, ks_now = ks_cur;
+          const float vs_now = vs, ks_now = ks;
           if (kv == 0) {
-            fetch(n + 1, raw[1], row_cur);
+            fetch(1, raw[1]);
           } else {
-            row_cur = row_next;
-            ks_cur = ks_next;
-            vs_cur = vs_next;
-            lookup(j + 2, row_next, ks_next, vs_next);
-            if (j + 1 < nt) fetch(n + 1, raw[0], row_cur);
+            place(j + 1, pg_next, in_next);
+            lookup(j + 2, pg_next, in_next);
+            if (j + 1 < nt) fetch(0, raw[0]);
           }
           if (n >= kTileSlots) {
             ok = mbar_wait_or(&sm.empty[slot], ((n / kTileSlots) - 1) & 1, &sm.dead);
@@ -525,25 +687,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
           }
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
-            const int r = i * kRowsPer + lane / kChunks, ch = lane % kChunks;
-            const float s = kv ? __shfl_sync(0xffffffffu, vs_now, r >> 2) : 1.f;
+            const int r = i * kRowsPer + lr;
             const uint4 x = raw[kv][i];
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             uint32_t b[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              b[2 * k] = scaled_bf16x2(dec::e4m3x2_f16x2(w[k]), s);
-              b[2 * k + 1] = scaled_bf16x2(dec::e4m3x2_f16x2_hi(w[k]), s);
+              b[2 * k] = dec::e4m3x2_f16x2(w[k]);
+              b[2 * k + 1] = dec::e4m3x2_f16x2_hi(w[k]);
             }
             uint8_t *tile = sm.ring[slot];
             *reinterpret_cast<uint4 *>(tile + tile_off(wl * kRowsWarp + r, 2 * ch)) = make_uint4(b[0], b[1], b[2], b[3]);
             *reinterpret_cast<uint4 *>(tile + tile_off(wl * kRowsWarp + r, 2 * ch + 1)) = make_uint4(b[4], b[5], b[6], b[7]);
           }
-          if (kv == 0) {
-            const float s = __shfl_sync(0xffffffffu, ks_now, lane >> 2);
-            sm.kscale[j & 3][wl * kRowsWarp + lane] = s * a.scale_log2;
+          if (kv == 0) {  // (the softmax reads both behind the scores of this step)
+            sm.kscale[j & 3][wl * kRowsWarp + lane] = __shfl_sync(0xffffffffu, ks_now, lane >> 2);
+            sm.vscale[j & 3][wl * kRowsWarp + lane] = __shfl_sync(0xffffffffu, vs_now, lane >> 2);
+            float v = fabsf(vs_now);
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+            if (lane == 0) sm.vmax[j & 3][wl] = v;
           }
-          pre::fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.full[slot]);
         }
@@ -552,7 +716,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
   }
   pre::tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     pre::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
