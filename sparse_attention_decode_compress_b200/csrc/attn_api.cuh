@@ -3,6 +3,8 @@
 // include/qsa.h).  Part of qsa_api.cu, whose launch and validation helpers it
 // uses.
 #pragma once
+#include <cudaTypedefs.h>
+
 #include "attn_common.cuh"
 #include "attn_decode.cuh"
 #include "attn_simple.cuh"
@@ -120,6 +122,37 @@ qsa_status launch_simple(const qsa::attn::Args &a, const AttnPlan &pl, long long
                 sizeof(qsa::attn::SimpleSmem<D>), s, a);
 }
 
+// The K/V caches for TMA: boxes of the largest power of two of rows, up to the
+// 32 that a loader warp fills, that divides the page size.  rows = 0 (the
+// kernel gathers every row) for fp8 caches, whose rows are converted, for pages
+// that are no multiple of 8 tokens, and where a row index passes 31 bits.
+qsa_status tile_maps(const qsa::attn::Args &a, qsa::attn::TileMaps &m) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  m.rows = 0;
+  const int P = a.c.page_size;
+  const long long rows = (long long)a.c.num_pages * P;
+  if (a.c.kv_dtype != QSA_BF16 || P % 8 != 0 || rows > 0x7fffffffLL) return QSA_OK;
+  if (!encode) return QSA_ERR_CUDA;
+  m.rows = P % 32 == 0 ? 32 : P % 16 == 0 ? 16 : 8;
+  const cuuint64_t D = a.c.head_dim, H = a.c.num_kv_heads;
+  const cuuint64_t dims[3] = {D, H, (cuuint64_t)rows}, strides[2] = {2 * D, 2 * D * H};
+  const cuuint32_t box[3] = {(cuuint32_t)qsa::attn::kBoxCols, 1, (cuuint32_t)m.rows}, ones[3] = {1, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (encode(i ? &m.v : &m.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(i ? a.c.v_cache : a.c.k_cache), dims, strides, box, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return QSA_ERR_CUDA;
+  return QSA_OK;
+}
+
 template <int MODE, int D, bool FP8>
 qsa_status launch_tile(const qsa::attn::Args &a, const AttnPlan &pl, long long seqs, cudaStream_t s) {
   static bool done[kMaxDevices] = {false};
@@ -129,8 +162,11 @@ qsa_status launch_tile(const qsa::attn::Args &a, const AttnPlan &pl, long long s
     std::lock_guard<std::mutex> lk(g_mutex);
     if (prepare_kernel(kernel, smem, done) != cudaSuccess) return QSA_ERR_CUDA;
   }
+  qsa::attn::TileMaps maps = {};
+  const qsa_status st = tile_maps(a, maps);
+  if (st != QSA_OK) return st;
   return launch(true, kernel, dim3((unsigned)pl.tiles, (unsigned)(a.c.num_kv_heads * pl.splits), (unsigned)seqs),
-                dim3(qsa::attn::kTileThreads), smem, s, a);
+                dim3(qsa::attn::kTileThreads), smem, s, a, maps);
 }
 
 // The rows of `seqs` sequences, as pl splits them.

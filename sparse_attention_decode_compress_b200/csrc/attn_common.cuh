@@ -20,9 +20,9 @@
 // The query heads of one kv head are rows of one small matrix: row
 // m = token * G + head-in-group of a sequence (G = Hq / Hkv), cut into tiles.
 // The keys a tile needs are one or two ranges, [0, sa) and [b0, b1); they are
-// walked as one VIRTUAL range [0, sa + b1 - b0).  sa and b0 are multiples of 4,
-// the page sizes too, so four virtual keys from a multiple of 4 on always lie
-// in one page.
+// walked as one VIRTUAL range [0, sa + b1 - b0).  sa and b0 are multiples of
+// `unit`, a power of two that divides the page size (4 at least), so `unit`
+// virtual keys from a multiple of it on always lie in one page.
 #pragma once
 #include "qsa_common.cuh"
 
@@ -153,7 +153,7 @@ struct Range {
   __device__ __forceinline__ int key(int x) const { return x < sa ? x : b0 + (x - sa); }
 };
 template <int MODE>
-__device__ __forceinline__ Range range_of(const Args &a, const Seq &q, int i0, int i1) {
+__device__ __forceinline__ Range range_of(const Args &a, const Seq &q, int i0, int i1, int unit = 4) {
   Range r;
   r.sa = r.b0 = r.n = 0;
   if (i1 <= i0) return r;
@@ -173,8 +173,8 @@ __device__ __forceinline__ Range range_of(const Args &a, const Seq &q, int i0, i
     record_error(kErrBounds);
     hi = (int)cap;
   }
-  sink = (min(sink, hi) + 3) & ~3;
-  lo &= ~3;
+  sink = (min(sink, hi) + unit - 1) & -unit;
+  lo &= -unit;
   if (lo >= hi) lo = hi;
   if (sink >= lo) {  // one range
     r.sa = 0;

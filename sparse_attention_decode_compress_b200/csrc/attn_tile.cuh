@@ -13,9 +13,12 @@
 //     tensor memory, running maximum and sum in registers, weights back to
 //     tensor memory in 16 bits, where the value product reads them as its A
 //     operand (they take the place of the scores)
-//   - warps 8-11       fill the ring of key and value tiles: rows are gathered
-//     page by page with 16-byte cp.async (any page size), fp8 rows are
-//     converted to f16 on the way
+//   - warps 8-11       fill the ring of key and value tiles, 32 rows each.  bf16
+//     rows of whole boxes come by TMA (pages of a multiple of 8 tokens);
+//     cp.async gathers the rest and zeroes rows that nothing sees.  (cp.async
+//     for everything: its 16-byte writes wait for the tensor core's operand
+//     reads, ~110 cycles an instruction, 3,500 a step, and the loaders bound the
+//     kernel.)  fp8 rows are converted to f16 on the way.
 //   - warp 12          one thread issues every product: values of a tile, then
 //     the scores of its next keys (warps 13-15 only complete the warpgroup that
 //     gives its registers to the softmax)
@@ -68,9 +71,17 @@ __device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t n) {
 __device__ __forceinline__ void mbar_arrive(uint64_t *b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
 }
-// Arrives when this thread's cp.async copies so far have landed.
-__device__ __forceinline__ void mbar_arrive_copies(uint64_t *b) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
+__device__ __forceinline__ void mbar_arrive_expect(uint64_t *b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+// A box of `kBoxCols` dims of one head, some rows, by TMA (128-byte swizzled).
+constexpr int kBoxCols = 64;
+__device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int col, int head, int row, uint64_t *b) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(col), "r"(head), "r"(row), "r"(smem_u32(b))
+      : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
   uint32_t ok;
@@ -314,9 +325,16 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first
   tmem_st_wait();
 }
 
+// The caches as TMA sees them, [token rows][Hkv][D] in boxes of `rows` tokens
+// (0: no TMA) that lie within a page.
+struct TileMaps {
+  CUtensorMap k, v;
+  int rows;
+};
+
 // Grid (row tiles of 256, Hkv * splits, sequences).
 template <int MODE, int D, bool FP8>
-__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
+__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, const __grid_constant__ TileMaps maps) {
   pdl_open();
   using SM = TileSmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -329,7 +347,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
   if (rows <= 0) return;
   const int g = blockIdx.y / a.splits, split = blockIdx.y - g * a.splits;
   const int i0 = m0 / a.G, i1 = (m0 + rows - 1) / a.G + 1;
-  const Range rg = range_of<MODE>(a, sq, i0, i1);
+  const Range rg = range_of<MODE>(a, sq, i0, i1, max(maps.rows, 4));
   const int x0 = split_bound(rg.n, a.splits, split, kTileKeys);
   const int x1 = split_bound(rg.n, a.splits, split + 1, kTileKeys);
   const int nt = (x1 - x0 + kTileKeys - 1) / kTileKeys;
@@ -343,7 +361,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
   }
   if (tid == 0) {
     // bf16: every loader thread's copies; fp8: every loader warp
-    constexpr uint32_t kArrivals = FP8 ? kTileLoaders : kTileLoaders * 32;
+    constexpr uint32_t kArrivals = kTileLoaders;
     for (int i = 0; i < kTileSlots; ++i) {
       mbar_init(&sm.full[i], kArrivals);
       mbar_init(&sm.empty[i], 1);
@@ -585,6 +603,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
     bool whole = false;  // every row of the warp's share is loaded
     int xw = 0;          // virtual key of its first row
     float ks = 0.f, vs = 0.f;  // fp8: scales of the keys' page
+    int tok_row = -1;          // lane i < 8: cache row of keys 4 i .. 4 i + 3
     auto place = [&](int j, int pg, int in_page) {
       long long row = -1;
       ks = vs = 0.f;
@@ -593,6 +612,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
           record_error(kErrBounds);
         } else {
           row = ((long long)pg * a.c.page_size + in_page) * row_stride;
+          tok_row = pg * a.c.page_size + in_page;  // (TMA: below 2^31)
           if (FP8) {
             ks = a.c.k_scale[(long long)pg * Hkv + g];
             vs = a.c.v_scale[(long long)pg * Hkv + g];
@@ -603,6 +623,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
       const int k0 = rg.key(xw), k1 = rg.key(xw + kRowsWarp - 1);
       whole = __all_sync(0xffffffffu, lane >= kRowsWarp / 4 || row >= 0) && xw + kRowsWarp <= x1 &&
               k1 - k0 == kRowsWarp - 1 && k1 < any.hi && (k0 >= any.lo || k1 < any.sink);
+      if (!FP8 && whole && maps.rows) return;  // TMA
 #pragma unroll
       for (int k = 0; k < kOffs; ++k) {
         const int at = kRowsPer == 2 ? k : kRowsPer == 4 ? k : 2 * k + (lr >> 2);
@@ -633,7 +654,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
     bool ok = true;
     if constexpr (!FP8) {
       // tile n of the ring: keys (n even) or values (n odd) of step n / 2
-      mbar_arrive_copies(&sm.qfull);
+      if (nt > 0) {
+        cp_async_wait<0>();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.qfull);
+      }
+      int behind = -1;  // slot whose copies by this warp are not announced yet
       for (int n = 0; n < 2 * nt; ++n) {
         const int j = n >> 1, slot = n % kTileSlots;
         if (n >= 2 && (n & 1) == 0) {
@@ -644,16 +670,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(Args a) {
           ok = mbar_wait_or(&sm.empty[slot], ((n / kTileSlots) - 1) & 1, &sm.dead);
           if (!__all_sync(0xffffffffu, ok)) break;
         }
+        if (whole && maps.rows) {
+          if (lane == 0) mbar_arrive_expect(&sm.full[slot], kRowsWarp * D * 2);
+          __syncwarp();
+          const int per = maps.rows >> 2;  // groups of four rows in a box
+          if (lane < kRowsWarp / 4 && (lane & (per - 1)) == 0) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          bool ld;
-          const uint8_t *src = source(i, n & 1, ld);
-          cp_async16_zfill(sm.ring[slot] + tile_off(wl * kRowsWarp + i * kRowsPer + lr, ch), src, ld);
+            for (int c = 0; c < D / kBoxCols; ++c)
+              tma_box(sm.ring[slot] + c * kColBlock + (wl * kRowsWarp + 4 * lane) * 128, n & 1 ? &maps.v : &maps.k,
+                      c * kBoxCols, g, tok_row, &sm.full[slot]);
+          }
+          if (behind >= 0) {
+            cp_async_wait<0>();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[behind]);
+            behind = -1;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            bool ld;
+            const uint8_t *src = source(i, n & 1, ld);
+            cp_async16_zfill(sm.ring[slot] + tile_off(wl * kRowsWarp + i * kRowsPer + lr, ch), src, ld);
+          }
+          cp_async_commit();
+          if (behind >= 0) {
+            cp_async_wait<1>();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[behind]);
+          }
+          behind = slot;
         }
-        mbar_arrive_copies(&sm.full[slot]);
       }
-      cp_async_commit();
       cp_async_wait<0>();
+      __syncwarp();
+      if (lane == 0 && behind >= 0) mbar_arrive(&sm.full[behind]);
     } else {
       // fp8: raw rows of the next tile are loaded while this one is converted
       uint4 raw[2][kLoads];

@@ -2,6 +2,7 @@
 // word, programmatic launch, cp.async, named barriers and L2 policies.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
