@@ -110,12 +110,14 @@ __device__ __forceinline__ bool mbar_wait_or(uint64_t *b, uint32_t parity, int *
   return true;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Products D (+)= A B: A in shared memory (a descriptor) or in tensor memory.
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
       :
-      : "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+      : "r"(d), "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -123,6 +125,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
       :
       : "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// One lane of the warp.  (elect.sync rather than a lane test: the products'
+// operands then stay in uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
 }
 
 #define QSA_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), \
@@ -478,28 +489,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ products --
     regs_down<kRegsMma>();
-    if (warp == kMmaWarp && lane == 0 && nt > 0) {
-      const uint32_t idesc_s = idesc_16(!FP8, kTileKeys, false), idesc_o = idesc_16(!FP8, D, true);
+    if (warp == kMmaWarp && nt > 0) {
+      constexpr uint32_t idesc_s = idesc_16(!FP8, kTileKeys, false), idesc_o = idesc_16(!FP8, D, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t q_desc = desc_k(smem_u32(sm.q)), k_desc = desc_k(smem_u32(sm.ring)),
+                     v_desc = desc_v(smem_u32(sm.ring));
+      constexpr uint32_t kTile16 = SM::kTile / 16;  // descriptors count 16 bytes
       auto scores = [&](int t, int slot) {
+        const uint64_t qd = q_desc + t * kTile16, kd = k_desc + slot * kTile16;
+        mma_ss<false>(tm + t * kTileKeys, qd, kd, idesc_s);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)(k / 4) * kColBlock + (uint32_t)(k % 4) * 32;
-          mma_ss(tmem + t * kTileKeys, desc_k(smem_u32(sm.q[t]) + off), desc_k(smem_u32(sm.ring[slot]) + off),
-                 idesc_s, k > 0);
+        for (int k = 1; k < D / 16; ++k) {
+          const uint32_t off = ((uint32_t)(k / 4) * kColBlock + (uint32_t)(k % 4) * 32) / 16;
+          mma_ss<true>(tm + t * kTileKeys, qd + off, kd + off, idesc_s);
         }
       };
       bool ok = mbar_wait_or(&sm.qfull, 0, &sm.dead) && mbar_wait_or(&sm.full[0], 0, &sm.dead);
+      ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         // what the loaders wrote goes over to the tensor core's view here, where
         // it is waited for: in the loaders the fence would wait for the copies
         // still in flight
         pre::fence_async_smem();
         pre::tc_fence_after();
-        for (int t = 0; t < tiles; ++t) {
-          scores(t, 0);
-          pre::umma_commit(&sm.sfull[t]);
+        if (elect_one()) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (t < tiles) {
+              scores(t, 0);
+              pre::umma_commit(&sm.sfull[t]);
+            }
+          pre::umma_commit(&sm.empty[0]);
         }
-        pre::umma_commit(&sm.empty[0]);
+        __syncwarp();
       }
       for (int j = 0; ok && j < nt; ++j) {
         const int nv = 2 * j + 1, nk = 2 * j + 2;  // this step's values, the next one's keys
@@ -507,24 +529,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
         ok = mbar_wait_or(&sm.full[nv % kTileSlots], (nv / kTileSlots) & 1, &sm.dead);
         if (ok && more) ok = mbar_wait_or(&sm.full[nk % kTileSlots], (nk / kTileSlots) & 1, &sm.dead);
         pre::fence_async_smem();
-        for (int t = 0; ok && t < tiles; ++t) {
-          ok = mbar_wait_or(&sm.pfull[t], j & 1, &sm.dead);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= tiles) break;
+          if (ok) ok = mbar_wait_or(&sm.pfull[t], j & 1, &sm.dead);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           pre::tc_fence_after();
+          if (elect_one()) {
+            const uint64_t vd = v_desc + (nv % kTileSlots) * kTile16;
 #pragma unroll
-          for (int k = 0; k < kTileKeys / 16; ++k)
-            mma_ts(tmem + 256 + t * 128, tmem + t * kTileKeys + 8 * k,
-                   desc_v(smem_u32(sm.ring[nv % kTileSlots]) + k * 2048), idesc_o, j > 0 || k > 0);
-          if (more) {
-            scores(t, nk % kTileSlots);
-            pre::umma_commit(&sm.sfull[t]);
-          } else {
-            pre::umma_commit(&sm.ofull[t]);
+            for (int k = 0; k < kTileKeys / 16; ++k)
+              mma_ts(tm + 256 + t * 128, tm + t * kTileKeys + 8 * k, vd + k * (2048 / 16), idesc_o,
+                     k > 0 ? 1u : (uint32_t)(j > 0));
+            if (more) {
+              scores(t, nk % kTileSlots);
+              pre::umma_commit(&sm.sfull[t]);
+            } else {
+              pre::umma_commit(&sm.ofull[t]);
+            }
+            if (t + 1 == tiles) {
+              pre::umma_commit(&sm.empty[nv % kTileSlots]);
+              if (more) pre::umma_commit(&sm.empty[nk % kTileSlots]);
+            }
           }
+          __syncwarp();
         }
-        if (!ok) break;
-        pre::umma_commit(&sm.empty[nv % kTileSlots]);
-        if (more) pre::umma_commit(&sm.empty[nk % kTileSlots]);
       }
     }
     __syncwarp();
