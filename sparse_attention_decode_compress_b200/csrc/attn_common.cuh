@@ -188,10 +188,11 @@ __device__ __forceinline__ Range range_of(const Args &a, const Seq &q, int i0, i
   return r;
 }
 
-// Split k of n virtual keys in `splits`: bounds at multiples of `unit`.
+// Split k of n virtual keys in `splits`: bounds at multiples of `unit`, the
+// splits alike to one unit.
 __device__ __forceinline__ int split_bound(int n, int splits, int k, int unit) {
-  const long long units = (n + unit - 1) / unit;
-  return (int)min((long long)n, units * k / splits * unit);
+  const int units = (int)(((unsigned)n + unit - 1) / unit), each = units / splits;
+  return min(n, (each * k + min(k, units - each * splits)) * unit);
 }
 
 __device__ __forceinline__ float ex2(float x) {

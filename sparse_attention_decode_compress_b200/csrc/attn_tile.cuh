@@ -22,11 +22,14 @@
 //   - warp 12          one thread issues every product: values of a tile, then
 //     the scores of its next keys (warps 13-15 only complete the warpgroup that
 //     gives its registers to the softmax)
-// The output accumulators stay in tensor memory.  They are rescaled only when
-// a row's maximum has grown by more than 2^8 since the last time (weights up to
-// 2^8 lose nothing in bf16 and float32), by the thread that owns the row: the
-// scores of step j are issued behind the values of step j - 1, so that thread
-// has them to itself between the two.
+// A step's weights are relative to the maximum of the steps BEFORE it: they
+// need not wait for their own (which runs beside them), and float32 and bf16
+// lose nothing by weights above 1.  When a row's maximum has grown by more than
+// 2^8 the next step starts with rescaling its sum and its output accumulators,
+// which stay in tensor memory; the scores of step j are issued behind the values
+// of step j - 1, so the thread that owns the row has them to itself then.  Only
+// growth beyond the weights' range (2^60; f16 weights: 2^13) makes 32 keys start
+// again with their own maximum.
 //
 // Rounding: weights to bf16, the error of the output's own rounding.  fp8
 // caches run in f16, which holds every E4M3 code: queries scaled per row by a
@@ -49,7 +52,7 @@ constexpr int kTileThreads = 16 * 32;
 constexpr int kLoadWarp = 8, kMmaWarp = 12;
 constexpr uint32_t kTmemCols = 512;  // S0, S1 at 0 and 128, O0, O1 at 256 and 384
 constexpr float kLazy = 8.f;    // growth of a row's maximum (log2) that is left in the weights
-constexpr unsigned long long kTileWaitNs = 2000000000ull;
+constexpr unsigned kTileTries = 1u << 25;
 
 template <int D>
 struct TileSmem {
@@ -94,14 +97,13 @@ __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase, at most kTileWaitNs; false when it ran out here or in
-// another role.
+// Waits for the phase for at most kTileTries tries (a second and more); false
+// when they ran out here or in another role.  (A clock read in the loop, the
+// global timer above all, put 500 cycles into every hand-over between roles.)
 __device__ __forceinline__ bool mbar_wait_or(uint64_t *b, uint32_t parity, int *dead) {
-  if (mbar_try(b, parity)) return true;
-  const unsigned long long t0 = pre::globaltimer();
-  while (!mbar_try(b, parity)) {
-    if (*reinterpret_cast<volatile int *>(dead)) return false;
-    if (pre::globaltimer() - t0 > kTileWaitNs) {
+  for (unsigned n = 0; !mbar_try(b, parity); ++n) {
+    if ((n & 1023u) == 1023u && *reinterpret_cast<volatile int *>(dead)) return false;
+    if (n >= kTileTries) {
       *reinterpret_cast<volatile int *>(dead) = 1;
       record_error(kErrTimeout);
       return false;
@@ -235,90 +237,104 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A row's weights of one step: the scores in tensor memory become weights
-// relative to the (possibly raised) maximum mx, the sum l and, when the
-// reference moves, the output accumulators follow.  see(c): the keys c .. c + 31
-// of the tile that the row sees, as bits (MASKED).
+// What a softmax thread keeps of its row: the maximum (scaled, log2) that sum
+// and outputs are relative to, the sum, the largest score so far, and (fp8) the
+// power of two that the value scales are relative to.
+struct RowState {
+  float mx, l, seen, vref;
+};
+
+// The row's sum and output accumulators over to reference `to` (and vref `ref`).
+template <int D, bool FP8>
+__device__ __forceinline__ void rebase(RowState &r, float to, float ref, bool first, uint32_t o_at) {
+  float al = to > r.mx ? (r.mx == -INFINITY ? 0.f : ex2(r.mx - to)) : 1.f;
+  r.l *= al;
+  r.mx = fmaxf(r.mx, to);
+  if (FP8) {
+    al *= ref > r.vref ? r.vref / ref : 1.f;
+    r.vref = fmaxf(r.vref, ref);
+  }
+  if (first) return;
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t v[16];
+    pre::tmem_ld16(o_at + c, v);
+    pre::tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+    tmem_st16(o_at + c, v);
+  }
+}
+
+// A row's weights of one step: the scores in tensor memory become weights and
+// the row's state follows.  see(c): the keys c .. c + 31 of the tile that the row
+// sees, as bits (MASKED).
 template <int D, bool FP8, bool MASKED, typename See>
 __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first, float scale, const float *ksc,
-                                        const float *vsc, const float *vmax, float &vref, float &mx, float &l,
-                                        See see) {
-  uint32_t s[4][32];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) tmem_ld32(s_at + 32 * q, s[q]);
-  pre::tmem_ld_wait();
-  float tops[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t bits = MASKED ? see(32 * q) : 0u;
-    if (FP8) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 k = *reinterpret_cast<const float4 *>(ksc + 32 * q + e);
-        s[q][e] = __float_as_uint(__uint_as_float(s[q][e]) * k.x);
-        s[q][e + 1] = __float_as_uint(__uint_as_float(s[q][e + 1]) * k.y);
-        s[q][e + 2] = __float_as_uint(__uint_as_float(s[q][e + 2]) * k.z);
-        s[q][e + 3] = __float_as_uint(__uint_as_float(s[q][e + 3]) * k.w);
-      }
-    }
-    if (MASKED) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!((bits >> e) & 1u)) s[q][e] = 0xff800000u;  // -inf
-    }
-    float t = __uint_as_float(s[q][0]);
-#pragma unroll
-    for (int e = 1; e < 31; e += 2) t = max3(t, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-    tops[q] = fmaxf(t, __uint_as_float(s[q][31]));
-  }
-  const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
-  const bool grow = top > mx + kLazy || (mx == -INFINITY && top > -INFINITY);
-  const float m_new = grow ? top : mx;
-  float al = grow ? (mx == -INFINITY ? 0.f : ex2(mx - m_new)) : 1.f;
-  l *= al;
-  bool move = grow;
+                                        const float *vsc, const float *vmax, RowState &r, See see) {
+  // ---- what the steps before left to do
+  float ref = r.vref;
   if (FP8) {
     const float4 w = *reinterpret_cast<const float4 *>(vmax);
     const float v = fmaxf(max3(w.x, w.y, w.z), w.w);
-    const float ref = dec::vs_binade(v);
-    if (v > 0.f && ref > vref) {
-      al *= vref / ref;
-      vref = ref;
-      move = true;
-    }
+    if (v > 0.f) ref = fmaxf(ref, dec::vs_binade(v));
   }
-  if (__any_sync(0xffffffffu, move) && !first) {
+  const float late = r.seen > r.mx + kLazy ? r.seen : r.mx;
+  if (__any_sync(0xffffffffu, late > r.mx || ref > r.vref)) rebase<D, FP8>(r, late, ref, first, o_at);
+
+  const f2 sc2 = pack2(scale, scale);
+  const float vinv = FP8 && r.vref > 0.f ? 1.f / r.vref : 0.f;
+  constexpr float kRange = FP8 ? 13.f : 60.f;
+  // the scores of keys c .. c + 31, -inf where the row does not see them
+  auto scores = [&](int c, uint32_t(&s)[32]) {
+    if (FP8) {
 #pragma unroll
-    for (int c = 0; c < D; c += 16) {
-      uint32_t v[16];
-      pre::tmem_ld16(o_at + c, v);
-      pre::tmem_ld_wait();
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-      tmem_st16(o_at + c, v);
+      for (int e = 0; e < 32; e += 4) {
+        const float4 k = *reinterpret_cast<const float4 *>(ksc + c + e);
+        s[e] = __float_as_uint(__uint_as_float(s[e]) * k.x);
+        s[e + 1] = __float_as_uint(__uint_as_float(s[e + 1]) * k.y);
+        s[e + 2] = __float_as_uint(__uint_as_float(s[e + 2]) * k.z);
+        s[e + 3] = __float_as_uint(__uint_as_float(s[e + 3]) * k.w);
+      }
     }
-  }
-  mx = m_new;
-  const float base = mx == -INFINITY ? 0.f : mx;
-  const f2 sc2 = pack2(scale, scale), nb2 = pack2(-base, -base);
-  const float vinv = FP8 && vref > 0.f ? 1.f / vref : 0.f;
-  f2 sum0 = 0, sum1 = 0;  // (0.f, 0.f)
+    if (MASKED) {
+      const uint32_t bits = see(c);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t p[16];
+      for (int e = 0; e < 32; ++e)
+        if (!((bits >> e) & 1u)) s[e] = 0xff800000u;
+    }
+  };
+  auto largest = [&](const uint32_t(&s)[32]) -> float {
+    float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[16]);
+#pragma unroll
+    for (int e = 1; e < 15; e += 2) {
+      t0 = max3(t0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+      t1 = max3(t1, __uint_as_float(s[16 + e]), __uint_as_float(s[17 + e]));
+    }
+    return fmaxf(max3(t0, t1, __uint_as_float(s[15])), __uint_as_float(s[31]));
+  };
+
+  float sum;
+  uint32_t p[16];
+  auto exps = [&](int c, const uint32_t(&s)[32]) {
+    const float base = r.mx == -INFINITY ? 0.f : r.mx;
+    const f2 nb2 = pack2(-base, -base);
+    f2 sum0 = 0, sum1 = 0;  // (0.f, 0.f)
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       float x0, x1, x2, x3;
-      unpack2(fma2(pack2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), sc2, nb2), x0, x1);
-      unpack2(fma2(pack2(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), sc2, nb2), x2, x3);
+      const f2 y0 = fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, nb2);
+      const f2 y1 = fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), sc2, nb2);
+      unpack2(y0, x0, x1);
       x0 = ex2(x0);
       x1 = ex2(x1);
+      unpack2(y1, x2, x3);
       x2 = ex2(x2);
       x3 = ex2(x3);
       sum0 = add2(sum0, pack2(x0, x1));
       sum1 = add2(sum1, pack2(x2, x3));
       if (FP8) {
-        const float4 v = *reinterpret_cast<const float4 *>(vsc + 32 * q + e);
+        const float4 v = *reinterpret_cast<const float4 *>(vsc + c + e);
         x0 *= v.x * vinv;
         x1 *= v.y * vinv;
         x2 *= v.z * vinv;
@@ -327,12 +343,51 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first
       p[e / 2] = pack16<!FP8>(x0, x1);
       p[e / 2 + 1] = pack16<!FP8>(x2, x3);
     }
+    float a, b;
+    unpack2(add2(sum0, sum1), a, b);
+    sum = a + b;
+  };
+  uint32_t s[2][32];
+  tmem_ld32(s_at, s[0]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    pre::tmem_ld_wait();
+    if (q < 3) tmem_ld32(s_at + 32 * (q + 1), s[(q + 1) & 1]);
+    scores(32 * q, s[q & 1]);
+    const float top = largest(s[q & 1]) * scale;
+    exps(32 * q, s[q & 1]);
+    if (__any_sync(0xffffffffu, top > r.mx + kRange)) {
+      // out of range (the first keys of every row): once more, relative to
+      // these keys' maximum; the weights in place follow
+      pre::tmem_ld_wait();
+      tmem_st_wait();
+      const float old = r.mx;
+      rebase<D, FP8>(r, top > r.mx ? top : r.mx, r.vref, first, o_at);
+      const float al = old == -INFINITY ? 0.f : ex2(old - r.mx);
+#pragma unroll 1
+      for (int k = 0; k < q; ++k) {
+        uint32_t w[16];
+        pre::tmem_ld16(s_at + 16 * k, w);
+        pre::tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float lo, hi;
+          if (FP8) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+            lo = f.x, hi = f.y;
+          } else {
+            lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
+          }
+          w[e] = pack16<!FP8>(lo * al, hi * al);
+        }
+        tmem_st16(s_at + 16 * k, w);
+      }
+      exps(32 * q, s[q & 1]);
+    }
+    r.seen = fmaxf(r.seen, top);
+    r.l += sum;
     tmem_st16(s_at + 16 * q, p);
   }
-  float a, b, c, d;
-  unpack2(sum0, a, b);
-  unpack2(sum1, c, d);
-  l += (a + b) + (c + d);
   tmem_st_wait();
 }
 
@@ -377,7 +432,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
       mbar_init(&sm.full[i], kArrivals);
       mbar_init(&sm.empty[i], 1);
     }
-    mbar_init(&sm.qfull, kArrivals);
+    mbar_init(&sm.qfull, kLoadWarp);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.sfull[t], 1);
       mbar_init(&sm.pfull[t], 4);
@@ -392,11 +447,49 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
   const uint32_t tmem = sm.tmem;
 
   // registers: 512 threads start with 128 each; the shares add up to that
-  constexpr int kRegsSoftmax = FP8 ? 176 : 192, kRegsLoad = FP8 ? 104 : 72, kRegsMma = 56;
+  constexpr int kRegsSoftmax = FP8 ? 152 : 168, kRegsLoad = FP8 ? 112 : 80, kRegsMma = 96;
   static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsMma <= 4 * 128, "register shares");
   if (warp < kLoadWarp) {
     // ------------------------------------------------------------ softmax --
     regs_up<kRegsSoftmax>();
+    // queries: bf16 rows, 2 D bytes
+    {
+      constexpr int kQ = D / 8;  // 16-byte chunks
+      const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(a.q);
+      for (int e = tid; e < tiles * kTileRows * kQ; e += kLoadWarp * 32) {
+        const int rr = e / kQ, ch = e % kQ, m = m0 + rr;
+        const bool ok = rr < rows;
+        const __nv_bfloat16 *src =
+            ok ? qg + ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D + ch * 8 : qg;
+        uint8_t *dst = sm.q[rr / kTileRows] + tile_off(rr % kTileRows, ch);
+        if constexpr (!FP8) {
+          cp_async16_zfill(dst, src, ok);
+        } else {
+          // f16, scaled so that 2^14 <= max |q| 2^e < 2^15; kQ lanes hold a row
+          const uint4 x = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t mxq = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mxq = max(mxq, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int off = kQ / 2; off >= 1; off >>= 1) mxq = max(mxq, __shfl_xor_sync(0xffffffffu, mxq, off));
+          const int ex = mxq == 0u ? 0 : min(141 - (int)(mxq >> 7), 126);
+          const float f = dec::pow2f(ex);
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = dec::pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
+          if (ch == 0) sm.qscale[rr] = dec::pow2f(-ex);
+        }
+      }
+      if (!FP8) {
+        cp_async_commit();
+        cp_async_wait<0>();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.qfull);
+    }
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int m = m0 + t * kTileRows + row;
@@ -412,8 +505,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
       vb = rg.sa + max(v.lo - rg.b0, 0);
       vc = min(rg.sa + v.hi - rg.b0, rg.n);
     }
-    float mx = -INFINITY, l = 0.f;  // maximum (scaled, log2) the weights are relative to, and their sum
-    float vref = 0.f;  // fp8: power of two that the value scales are relative to
+    RowState r = {-INFINITY, 0.f, -INFINITY, 0.f};
     bool ok = true;
     if (t < tiles) {
       float scale = a.scale_log2;
@@ -434,11 +526,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
           return below(va - x) | (below(vc - x) & ~below(vb - x));
         };
         if (masked)
-          weights<D, FP8, true>(s_at, o_at, j == 0, scale, sm.kscale[j & 3], sm.vscale[j & 3], sm.vmax[j & 3], vref,
-                                mx, l, see);
+          weights<D, FP8, true>(s_at, o_at, j == 0, scale, sm.kscale[j & 3], sm.vscale[j & 3], sm.vmax[j & 3], r, see);
         else
-          weights<D, FP8, false>(s_at, o_at, j == 0, scale, sm.kscale[j & 3], sm.vscale[j & 3], sm.vmax[j & 3], vref,
-                                 mx, l, see);
+          weights<D, FP8, false>(s_at, o_at, j == 0, scale, sm.kscale[j & 3], sm.vscale[j & 3], sm.vmax[j & 3], r, see);
         pre::tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pfull[t]);
@@ -447,9 +537,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
       if (ok && nt > 0) ok = mbar_wait_or(&sm.ofull[t], 0, &sm.dead);
       ok = __all_sync(0xffffffffu, ok);
       pre::tc_fence_after();
-      const bool some = l != 0.f;  // (a NaN sum stays one)
-      const float inv = some ? (FP8 ? vref / l : 1.f / l) : 0.f;
-      const float lse = some ? ((mx == -INFINITY ? 0.f : mx) + __log2f(l)) * kLn2 : -INFINITY;
+      const bool some = r.l != 0.f;  // (a NaN sum stays one)
+      const float inv = some ? (FP8 ? r.vref / r.l : 1.f / r.l) : 0.f;
+      const float lse = some ? ((r.mx == -INFINITY ? 0.f : r.mx) + __log2f(r.l)) * kLn2 : -INFINITY;
       const long long at = (long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G;
       const long long slot = at * a.slots + a.slot0 + split;
       if (ok) {
@@ -489,71 +579,60 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ products --
     regs_down<kRegsMma>();
-    if (warp == kMmaWarp && nt > 0) {
+    // (one elected thread runs the whole role: its operands stay in uniform
+    // registers, and a wait that is over costs it few cycles)
+    if (warp == kMmaWarp && nt > 0 && elect_one()) {
       constexpr uint32_t idesc_s = idesc_16(!FP8, kTileKeys, false), idesc_o = idesc_16(!FP8, D, true);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t q_desc = desc_k(smem_u32(sm.q)), k_desc = desc_k(smem_u32(sm.ring)),
                      v_desc = desc_v(smem_u32(sm.ring));
       constexpr uint32_t kTile16 = SM::kTile / 16;  // descriptors count 16 bytes
       auto scores = [&](int t, int slot) {
         const uint64_t qd = q_desc + t * kTile16, kd = k_desc + slot * kTile16;
-        mma_ss<false>(tm + t * kTileKeys, qd, kd, idesc_s);
+        mma_ss<false>(tmem + t * kTileKeys, qd, kd, idesc_s);
 #pragma unroll
         for (int k = 1; k < D / 16; ++k) {
           const uint32_t off = ((uint32_t)(k / 4) * kColBlock + (uint32_t)(k % 4) * 32) / 16;
-          mma_ss<true>(tm + t * kTileKeys, qd + off, kd + off, idesc_s);
+          mma_ss<true>(tmem + t * kTileKeys, qd + off, kd + off, idesc_s);
         }
+        pre::umma_commit(&sm.sfull[t]);
       };
-      bool ok = mbar_wait_or(&sm.qfull, 0, &sm.dead) && mbar_wait_or(&sm.full[0], 0, &sm.dead);
-      ok = __all_sync(0xffffffffu, ok);
+      auto filled = [&](int n) { return mbar_wait_or(&sm.full[n % kTileSlots], (n / kTileSlots) & 1, &sm.dead); };
+      bool ok = mbar_wait_or(&sm.qfull, 0, &sm.dead) && filled(0);
       if (ok) {
         // what the loaders wrote goes over to the tensor core's view here, where
         // it is waited for: in the loaders the fence would wait for the copies
         // still in flight
         pre::fence_async_smem();
-        pre::tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (t < tiles) {
-              scores(t, 0);
-              pre::umma_commit(&sm.sfull[t]);
-            }
-          pre::umma_commit(&sm.empty[0]);
-        }
-        __syncwarp();
+        scores(0, 0);
+        if (tiles > 1) scores(1, 0);
+        pre::umma_commit(&sm.empty[0]);
+        ok = filled(1) && (nt == 1 || filled(2));
+        pre::fence_async_smem();
       }
       for (int j = 0; ok && j < nt; ++j) {
         const int nv = 2 * j + 1, nk = 2 * j + 2;  // this step's values, the next one's keys
         const bool more = j + 1 < nt;
-        ok = mbar_wait_or(&sm.full[nv % kTileSlots], (nv / kTileSlots) & 1, &sm.dead);
-        if (ok && more) ok = mbar_wait_or(&sm.full[nk % kTileSlots], (nk / kTileSlots) & 1, &sm.dead);
-        pre::fence_async_smem();
+        const uint64_t vd = v_desc + (nv % kTileSlots) * kTile16;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (t >= tiles) break;
-          if (ok) ok = mbar_wait_or(&sm.pfull[t], j & 1, &sm.dead);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = mbar_wait_or(&sm.pfull[t], j & 1, &sm.dead);
           if (!ok) break;
           pre::tc_fence_after();
-          if (elect_one()) {
-            const uint64_t vd = v_desc + (nv % kTileSlots) * kTile16;
 #pragma unroll
-            for (int k = 0; k < kTileKeys / 16; ++k)
-              mma_ts(tm + 256 + t * 128, tm + t * kTileKeys + 8 * k, vd + k * (2048 / 16), idesc_o,
-                     k > 0 ? 1u : (uint32_t)(j > 0));
-            if (more) {
-              scores(t, nk % kTileSlots);
-              pre::umma_commit(&sm.sfull[t]);
-            } else {
-              pre::umma_commit(&sm.ofull[t]);
-            }
-            if (t + 1 == tiles) {
-              pre::umma_commit(&sm.empty[nv % kTileSlots]);
-              if (more) pre::umma_commit(&sm.empty[nk % kTileSlots]);
-            }
-          }
-          __syncwarp();
+          for (int k = 0; k < kTileKeys / 16; ++k)
+            mma_ts(tmem + 256 + t * 128, tmem + t * kTileKeys + 8 * k, vd + k * (2048 / 16), idesc_o,
+                   k > 0 ? 1u : (uint32_t)(j > 0));
+          if (more) scores(t, nk % kTileSlots);
+          else pre::umma_commit(&sm.ofull[t]);
+        }
+        if (!ok) break;
+        pre::umma_commit(&sm.empty[nv % kTileSlots]);
+        if (more) {
+          pre::umma_commit(&sm.empty[nk % kTileSlots]);
+          // the next step's tiles, while this one's products run
+          ok = filled(nv + 2) && (j + 2 == nt || filled(nk + 2));
+          pre::fence_async_smem();
         }
       }
     }
@@ -571,39 +650,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
     const long long row_stride = (long long)Hkv * kRowBytes;
     const uint8_t *base[2] = {static_cast<const uint8_t *>(a.c.k_cache) + (long long)g * kRowBytes,
                               static_cast<const uint8_t *>(a.c.v_cache) + (long long)g * kRowBytes};
-    // queries: bf16 rows, 2 D bytes
-    {
-      constexpr int kQ = D / 8;  // 16-byte chunks
-      const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(a.q);
-      for (int e = wl * 32 + lane; e < tiles * kTileRows * kQ; e += kTileLoaders * 32) {
-        const int rr = e / kQ, ch = e % kQ, m = m0 + rr;
-        const bool ok = rr < rows;
-        const __nv_bfloat16 *src =
-            ok ? qg + ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D + ch * 8 : qg;
-        uint8_t *dst = sm.q[rr / kTileRows] + tile_off(rr % kTileRows, ch);
-        if constexpr (!FP8) {
-          cp_async16_zfill(dst, src, ok);
-        } else {
-          // f16, scaled so that 2^14 <= max |q| 2^e < 2^15; kQ lanes hold a row
-          const uint4 x = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t mxq = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mxq = max(mxq, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-#pragma unroll
-          for (int off = kQ / 2; off >= 1; off >>= 1) mxq = max(mxq, __shfl_xor_sync(0xffffffffu, mxq, off));
-          const int ex = mxq == 0u ? 0 : min(141 - (int)(mxq >> 7), 126);
-          const float f = dec::pow2f(ex);
-          uint32_t h[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = dec::pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-          if (ch == 0) sm.qscale[rr] = dec::pow2f(-ex);
-        }
-      }
-      cp_async_commit();
-    }
     // keys that some row of the CTA sees; the others are zero
     Seen any = seen_by<MODE>(a, sq, i1 - 1);
     if (MODE == kWindow) any.lo = max(0, sq.first + i0 + 1 - a.window);
@@ -684,11 +730,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
     bool ok = true;
     if constexpr (!FP8) {
       // tile n of the ring: keys (n even) or values (n odd) of step n / 2
-      if (nt > 0) {
-        cp_async_wait<0>();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.qfull);
-      }
       int behind = -1;  // slot whose copies by this warp are not announced yet
       for (int n = 0; n < 2 * nt; ++n) {
         const int j = n >> 1, slot = n % kTileSlots;
@@ -747,8 +788,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
         }
       };
       if (nt > 0) fetch(0, raw[0]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.qfull);
       for (int j = 0; j < nt && ok; ++j) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
