@@ -35,7 +35,7 @@ AttnPlan plan_simple(long long seqs, int Hkv, long long rows, long long span) {
   AttnPlan p;
   p.tiles = ceil_ll(std::max(rows, 1LL), qsa::attn::kSimpleRows);
   const long long ctas = std::max(1LL, seqs * Hkv * p.tiles);
-  p.splits = (int)std::max(1LL, std::min({4LL * kPlanSMs / ctas, ceil_ll(span, 4 * qsa::attn::kSimpleKeys), 64LL}));
+  p.splits = (int)std::max(1LL, std::min({4LL * kPlanSMs / ctas, ceil_ll(span, 2 * qsa::attn::kSimpleKeys), 64LL}));
   return p;
 }
 
@@ -117,9 +117,15 @@ void set_parts(qsa::attn::Args &a, int slots, void *workspace) {
 // ----------------------------------------------------------------- launch --
 template <int MODE, int D>
 qsa_status launch_simple(const qsa::attn::Args &a, const AttnPlan &pl, long long seqs, cudaStream_t s) {
+  static bool done[kMaxDevices] = {false};
+  auto kernel = qsa::attn::simple_kernel<MODE, D>;
+  const size_t smem = sizeof(qsa::attn::SimpleSmem<D>);
+  {
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if (prepare_kernel(kernel, smem, done) != cudaSuccess) return QSA_ERR_CUDA;
+  }
   const dim3 grid((unsigned)pl.tiles, (unsigned)(a.c.num_kv_heads * pl.splits), (unsigned)seqs);
-  return launch(true, qsa::attn::simple_kernel<MODE, D>, grid, dim3(qsa::attn::kSimpleThreads),
-                sizeof(qsa::attn::SimpleSmem<D>), s, a);
+  return launch(true, kernel, grid, dim3(qsa::attn::kSimpleThreads), smem, s, a);
 }
 
 // The K/V caches for TMA: boxes of the largest power of two of rows, up to the
@@ -221,15 +227,20 @@ qsa_status launch_decode_rows(qsa::attn::Args a, const AttnPlan &pl, int slot0, 
   return fp8 ? launch_stream_nt<MODE, 128, true>(a, pl, s) : launch_stream_nt<MODE, 128, false>(a, pl, s);
 }
 
-qsa_status launch_attn_merge(const qsa::attn::Args &a, cudaStream_t s) {
+template <int W>
+qsa_status launch_attn_merge_w(const qsa::attn::Args &a, cudaStream_t s) {
   using namespace qsa::attn;
-  const long long warps = (long long)a.n_tok * a.Hq;
-  const long long grid = ceil_ll(warps * 32, kMergeThreads);
+  const long long rows = (long long)a.n_tok * a.Hq, grid = W == 1 ? ceil_ll(rows, kMergeWarps) : rows;
   if (grid > 0x7fffffffLL) return QSA_ERR_UNSUPPORTED;
   const bool f32 = a.c.kv_dtype == QSA_F32;
-  auto k = a.c.head_dim == 64 ? (f32 ? merge_kernel<64, float> : merge_kernel<64, __nv_bfloat16>)
-                              : (f32 ? merge_kernel<128, float> : merge_kernel<128, __nv_bfloat16>);
+  auto k = a.c.head_dim == 64 ? (f32 ? merge_kernel<64, float, W> : merge_kernel<64, __nv_bfloat16, W>)
+                              : (f32 ? merge_kernel<128, float, W> : merge_kernel<128, __nv_bfloat16, W>);
   return launch(true, k, dim3((unsigned)grid), dim3(kMergeThreads), 0, s, a);
+}
+
+qsa_status launch_attn_merge(const qsa::attn::Args &a, cudaStream_t s) {
+  return a.slots <= qsa::attn::kMergeFew ? launch_attn_merge_w<1>(a, s)
+                                         : launch_attn_merge_w<qsa::attn::kMergeWarps>(a, s);
 }
 
 AttnPlan plan_decode(const qsa_cache *c, int B, int T, int Hq, long long window, long long sinks) {

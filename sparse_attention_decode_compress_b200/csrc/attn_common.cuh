@@ -212,46 +212,87 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v) {
   *reinterpret_cast<uint2 *>(p) = w;
 }
 
-// Merge of the partial results of every (token, head) row, one warp each:
+// Merge of the partial results of every (token, head) row:
 //   lse = log sum_k exp(lse_k),  o = sum_k exp(lse_k - lse) o_k,
-// o = 0 and lse = -inf for a row that saw nothing.  Slots are added in order,
-// so a result does not depend on how the work was scheduled.
+// o = 0 and lse = -inf for a row that saw nothing.  W warps share a row, each
+// taking every W-th slot (lane i its i-th): one for up to 16 slots, four, whose
+// sums meet in shared memory, for up to 128.  A warp's weights are made lane by
+// lane and its rows loaded eight at a time: latency bounds this (one slot after
+// the other took 39 us for 65 slots of 512 rows).  Slots are added in a fixed
+// order, so a result does not depend on how the work was scheduled.
 constexpr int kMergeThreads = 128;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeFew = 16;
+constexpr int kMaxSlots = 32 * kMergeWarps;
 
-template <int D, typename OutT>
+template <int D, typename OutT, int W>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(Args a) {
   pdl_open();
-  const long long row = ((long long)blockIdx.x * kMergeThreads + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = W == 1 ? (long long)blockIdx.x * kMergeWarps + warp : (long long)blockIdx.x;
   if (row >= (long long)a.n_tok * a.Hq) return;
   if (a.cu && a.prefix_lens == nullptr && row / a.Hq >= a.cu[a.n_cu]) return;  // rows behind the last sequence
-  const int S = a.slots;
-  const float *lp = a.lse_part + row * S;
-  float mx = -INFINITY;
-  bool nan = false;
-  for (int k = lane; k < S; k += 32) {
-    const float l = __ldcg(lp + k);
-    nan |= l != l;
-    mx = fmaxf(mx, l);
-  }
+  const int S = a.slots, w0 = W == 1 ? 0 : warp;
+  const int mine = lane * W + w0;  // this lane's slot
+  const float l = mine < S ? __ldcg(a.lse_part + row * S + mine) : -INFINITY;
+  float mx = l;
+  bool nan = l != l;
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  if (__any_sync(0xffffffffu, nan)) mx = NAN;  // a NaN in any part is one in the result
+  nan = __any_sync(0xffffffffu, nan);
+  __shared__ float red_mx[kMergeWarps], red_z[kMergeWarps], red_o[W == 1 ? 1 : kMergeWarps][D];
+  if (W > 1) {
+    if (lane == 0) red_mx[warp] = nan ? NAN : mx;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      mx = fmaxf(mx, red_mx[i]);
+      nan |= red_mx[i] != red_mx[i];
+    }
+  }
+  if (nan) mx = NAN;  // a NaN in any part is one in the result
+  const float wt = (l == -INFINITY && !nan) ? 0.f : __expf(l - mx);
+  float z = mine < S ? wt : 0.f;
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float z = 0.f;
-  const int d = 4 * lane;
-  if (mx != -INFINITY) {
-    for (int k = 0; k < S; ++k) {
-      const float l = __ldcg(lp + k);
-      if (l == -INFINITY) continue;
-      const float w = __expf(l - mx);
-      z += w;
+  const int d = 4 * lane, n = (S - w0 + W - 1) / W;  // slots of this warp
+  const float4 *src = reinterpret_cast<const float4 *>(a.o_part + (row * S + w0) * D + d);
+  for (int k0 = 0; k0 < n; k0 += 8) {
+    float4 v[8];
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      f[k] = __shfl_sync(0xffffffffu, wt, (k0 + k) & 31);
+      // (an empty slot's row was not written)
+      v[k] = (k0 + k < n && f[k] != 0.f && d < D) ? __ldcg(src + (long long)(k0 + k) * W * (D / 4))
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k0 + k >= n || f[k] == 0.f) continue;
+      acc.x = __fmaf_rn(f[k], v[k].x, acc.x);
+      acc.y = __fmaf_rn(f[k], v[k].y, acc.y);
+      acc.z = __fmaf_rn(f[k], v[k].z, acc.z);
+      acc.w = __fmaf_rn(f[k], v[k].w, acc.w);
+    }
+  }
+  if (W > 1) {
+    if (d < D) *reinterpret_cast<float4 *>(&red_o[warp][d]) = acc;
+    if (lane == 0) red_z[warp] = z;
+    __syncthreads();
+    if (warp > 0) return;
+    z = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      z += red_z[i];
       if (d < D) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.o_part + (row * S + k) * D + d));
-        acc.x = __fmaf_rn(w, v.x, acc.x);
-        acc.y = __fmaf_rn(w, v.y, acc.y);
-        acc.z = __fmaf_rn(w, v.z, acc.z);
-        acc.w = __fmaf_rn(w, v.w, acc.w);
+        const float4 v = *reinterpret_cast<const float4 *>(&red_o[i][d]);
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
       }
     }
   }

@@ -25,6 +25,11 @@ constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kStageKeys = 16;
 constexpr int kMetaKeys = 128;  // keys whose pages a warp looks up at once: 4 a lane
 
+// Growth of a column's scores (log2) over its reference that is left in the
+// weights (below 2^8, which bf16, f16 and float32 hold as exactly as 1): the
+// lanes then need not agree on a maximum at every stage.
+constexpr float kDecLazy = 8.f;
+
 // Stages of a warp's ring: 96 KB (bf16) or 64 KB (fp8) of shared memory a CTA
 // at D = 128, two and three CTAs an SM.
 template <bool FP8>
@@ -248,37 +253,62 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
         v1 = __shfl_sync(0xffffffffu, vs_cur, at + 2) * inv;
       }
       uint32_t pb[NT][2];
-      float alpha[NT][2];
-      bool rescale = false;
+      float y[NT][4];
+      bool grow = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[j][e] = (sacc[j][e] + sac2[j][e]) * csc[j][e];
+          y[j][2 + e] = (sacc[j][2 + e] + sac2[j][2 + e]) * csc[j][e];
+          if constexpr (FP8) {
+            y[j][e] *= f0;
+            y[j][2 + e] *= f1;
+          }
+          if (!whole) {
+            const bool in0 = k0 < rhi[j][e] && (k0 >= rlo[j][e] || k0 < rsink) && xk < w1;
+            const bool in1 = k1 < rhi[j][e] && (k1 >= rlo[j][e] || k1 < rsink) && xk + 8 < w1;
+            if (!in0) y[j][e] = -INFINITY;
+            if (!in1) y[j][2 + e] = -INFINITY;
+          }
+          grow |= fmaxf(y[j][e], y[j][2 + e]) > mcol[j][e] + kDecLazy;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        // some column's scores outgrew its reference (its first keys do):
+        // the columns' maxima over the lanes, and what is summed follows
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float alpha[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(y[j][e], y[j][2 + e]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float m_new = fmaxf(mcol[j][e], mx);
+            alpha[e] = m_new == mcol[j][e] ? 1.f : mcol[j][e] == -INFINITY ? 0.f : attn::ex2(mcol[j][e] - m_new);
+            mcol[j][e] = m_new;
+            lcol[j][e] *= alpha[e];
+          }
+#pragma unroll
+          for (int i = 0; i < MD; ++i) {
+            o[i][j][0] *= alpha[0];
+            o[i][j][1] *= alpha[1];
+            o[i][j][2] *= alpha[0];
+            o[i][j][3] *= alpha[1];
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float y0 = (sacc[j][e] + sac2[j][e]) * csc[j][e], y1 = (sacc[j][2 + e] + sac2[j][2 + e]) * csc[j][e];
-          if constexpr (FP8) {
-            y0 *= f0;
-            y1 *= f1;
-          }
-          if (!whole) {
-            const bool in0 = k0 < rhi[j][e] && (k0 >= rlo[j][e] || k0 < rsink) && xk < w1;
-            const bool in1 = k1 < rhi[j][e] && (k1 >= rlo[j][e] || k1 < rsink) && xk + 8 < w1;
-            if (!in0) y0 = -INFINITY;
-            if (!in1) y1 = -INFINITY;
-          }
-          float mx = fmaxf(y0, y1);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float m_new = fmaxf(mcol[j][e], mx);
-          const float base = m_new == -INFINITY ? 0.f : m_new;
-          const float al = m_new == -INFINITY ? 1.f : attn::ex2(mcol[j][e] - base);
-          alpha[j][e] = al;
-          rescale |= al != 1.f;
-          mcol[j][e] = m_new;
-          p[e] = attn::ex2(y0 - base);
-          p[2 + e] = attn::ex2(y1 - base);
-          lcol[j][e] = lcol[j][e] * al + p[e] + p[2 + e];
+          const float base = mcol[j][e] == -INFINITY ? 0.f : mcol[j][e];
+          p[e] = attn::ex2(y[j][e] - base);
+          p[2 + e] = attn::ex2(y[j][2 + e] - base);
+          lcol[j][e] += p[e] + p[2 + e];
         }
         if constexpr (FP8) {
           pb[j][0] = movmatrix_t(pack_f16(p[0] * v0, p[1] * v0));
@@ -287,17 +317,6 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
           pb[j][0] = movmatrix_t(pack_bf16(p[0], p[1]));
           pb[j][1] = movmatrix_t(pack_bf16(p[2], p[3]));
         }
-      }
-      if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-        for (int i = 0; i < MD; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            o[i][j][0] *= alpha[j][0];
-            o[i][j][1] *= alpha[j][1];
-            o[i][j][2] *= alpha[j][0];
-            o[i][j][3] *= alpha[j][1];
-          }
       }
       // ---- O^T += V^T P^T
       if constexpr (FP8) {

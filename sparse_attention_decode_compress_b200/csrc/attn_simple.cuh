@@ -3,7 +3,8 @@
 //
 // One CTA of 4 warps takes a tile of 16 query rows of one sequence and kv
 // head and one split of its keys.  32 keys at a time are staged in shared
-// memory; a lane owns a key for the scores (its row padded against bank
+// memory (cp.async, the next tile in flight while one is computed, its pages
+// looked up one more tile ahead); a lane owns a key for the scores (its row padded against bank
 // conflicts) and a slice of the head dimension for the values, a warp owns 4
 // query rows, and the softmax runs online (running maximum and sum).
 #pragma once
@@ -19,8 +20,8 @@ constexpr int kSimpleKeys = 32;
 template <int D>
 struct SimpleSmem {
   float q[kSimpleRows][D];
-  float k[kSimpleKeys][D + 4];
-  float v[kSimpleKeys][D];
+  float k[2][kSimpleKeys][D + 4];
+  float v[2][kSimpleKeys][D];
 };
 
 __device__ __forceinline__ float4 load4(const void *p, long long at) {
@@ -69,32 +70,51 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
     for (int i = 0; i < kDims; ++i) o[j][i] = 0.f;
   }
 
-  for (int xt = x0; xt < x1; xt += kSimpleKeys) {
-    __syncthreads();  // the tile before is read
-    for (int e = tid; e < kSimpleKeys * kVec; e += kSimpleThreads) {
-      const int j = e / kVec, d = e % kVec * 4, x = xt + j;
-      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-      if (x < x1) {
-        const int key = rg.key(x);
-        const int lp = key / a.c.page_size;
-        const int pg = physical_page(a.c, sq.table, lp);
-        if (pg >= 0) {
-          const long long at =
-              (((long long)pg * a.c.page_size + (key - lp * a.c.page_size)) * a.c.num_kv_heads + g) * D + d;
-          kv = load4(a.c.k_cache, at);
-          vv = load4(a.c.v_cache, at);
-        }
+  // ---- loads: a warp owns the keys warp, warp + 4, .. of a tile; lane i < 8
+  // holds the cache row of the i-th of them (-1: zeros)
+  constexpr int kOwn = kSimpleKeys / 4;
+  auto lookup = [&](int xt) -> long long {
+    const int x = xt + warp + 4 * lane;
+    if (lane >= kOwn || x >= x1) return -1;
+    const int key = rg.key(x), lp = key / a.c.page_size;
+    const int pg = physical_page(a.c, sq.table, lp);
+    return pg < 0 ? -1 : (long long)pg * a.c.page_size + (key - lp * a.c.page_size);
+  };
+  const float *kbase = static_cast<const float *>(a.c.k_cache) + (long long)g * D;
+  const float *vbase = static_cast<const float *>(a.c.v_cache) + (long long)g * D;
+  auto issue = [&](int buf, long long row) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int j = warp + 4 * i;
+      const long long r = __shfl_sync(0xffffffffu, row, i);
+      const long long at = r * a.c.num_kv_heads * D + 4 * (lane % kVec);
+      if (lane < kVec) {
+        cp_async16_zfill(&sm.k[buf][j][4 * lane], r >= 0 ? kbase + at : kbase, r >= 0);
+        cp_async16_zfill(&sm.v[buf][j][4 * lane], r >= 0 ? vbase + at : vbase, r >= 0);
       }
-      *reinterpret_cast<float4 *>(&sm.k[j][d]) = kv;
-      *reinterpret_cast<float4 *>(&sm.v[j][d]) = vv;
     }
+  };
+  long long ahead = -1;
+  if (x0 < x1) {
+    issue(0, lookup(x0));
+    ahead = lookup(x0 + kSimpleKeys);
+  }
+  cp_async_commit();
+  int buf = 0;
+  for (int xt = x0; xt < x1; xt += kSimpleKeys, buf ^= 1) {
+    if (xt + kSimpleKeys < x1) {
+      issue(buf ^ 1, ahead);
+      ahead = lookup(xt + 2 * kSimpleKeys);
+    }
+    cp_async_commit();
+    cp_async_wait<1>();
     __syncthreads();
     float s[kRowsPerWarp];
 #pragma unroll
     for (int j = 0; j < kRowsPerWarp; ++j) s[j] = 0.f;
 #pragma unroll 8
     for (int d = 0; d < D; d += 4) {
-      const float4 k = *reinterpret_cast<const float4 *>(&sm.k[lane][d]);
+      const float4 k = *reinterpret_cast<const float4 *>(&sm.k[buf][lane][d]);
 #pragma unroll
       for (int j = 0; j < kRowsPerWarp; ++j) {
         const float4 q = *reinterpret_cast<const float4 *>(&sm.q[warp * kRowsPerWarp + j][d]);
@@ -123,15 +143,17 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
     for (int t = 0; t < kSimpleKeys; ++t) {
       float v[kDims];
 #pragma unroll
-      for (int i = 0; i < kDims; ++i) v[i] = sm.v[t][lane + 32 * i];
+      for (int i = 0; i < kDims; ++i) v[i] = sm.v[buf][t][lane + 32 * i];
 #pragma unroll
       for (int j = 0; j < kRowsPerWarp; ++j) {
         const float p = __shfl_sync(0xffffffffu, s[j], t);
 #pragma unroll
-        for (int i = 0; i < kDims; ++i) o[j][i] = p > 0.f ? fmaf(p, v[i], o[j][i]) : o[j][i];
+        for (int i = 0; i < kDims; ++i) o[j][i] = p != 0.f ? fmaf(p, v[i], o[j][i]) : o[j][i];
       }
     }
+    __syncthreads();  // the buffer is read
   }
+  cp_async_wait<0>();
 
 #pragma unroll
   for (int j = 0; j < kRowsPerWarp; ++j) {
