@@ -11,59 +11,73 @@ device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
 import torch
 
 from . import _lib
-from .api import _KV_DTYPES, QSACache, _check, _need, new_workspace
+from .api import QSACache, _check, _need, new_workspace
 
 _Q_DTYPES = {torch.float32: _lib.QSA_F32, torch.bfloat16: _lib.QSA_BF16}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-_HERE = contextlib.nullcontext()
 
 
-def _device(index: int):
-    """The caches' device as the current one, for the launch."""
-    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+class _Caches:
+    """What every call takes from the caches, found once: the C struct (and a
+    reference to it), the device index, the query type and the head shape."""
+    __slots__ = ("struct", "ref", "index", "dtype", "qd", "Hkv", "D", "device")
+
+    def __init__(self, cache: QSACache):
+        self.struct = cache.struct()
+        self.ref = ctypes.byref(self.struct)
+        self.device = cache.k_cache.device
+        self.index = cache.k_cache.get_device()
+        self.dtype = torch.float32 if cache.k_cache.dtype == torch.float32 else torch.bfloat16
+        self.qd = _Q_DTYPES[self.dtype]
+        _, _, self.Hkv, self.D = cache.k_cache.shape
 
 
-def _stream(stream, index: int) -> int:
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(index).cuda_stream
+def _call(fn, name: str, index: int, args: tuple, stream) -> None:
+    """fn(*args, stream) with the caches' device as the current one."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call(fn, name, index, args, stream)
+    handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    status = fn(*args, handle)
+    if status:
+        _check(status, name)
 
 
-def _query_type(cache: QSACache) -> torch.dtype:
-    if cache.k_cache.dtype not in _KV_DTYPES:
-        raise TypeError("k_cache must be float32, bfloat16 or float8_e4m3fn")
-    return torch.float32 if cache.k_cache.dtype == torch.float32 else torch.bfloat16
-
-
-def _ints(t: torch.Tensor, n: int, name: str, device: torch.device) -> int:
-    if t.dtype != torch.int32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
+def _ints(t: torch.Tensor, n: int, name: str, index: int) -> int:
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the cache's device")
     return t.data_ptr()
 
 
-def _dense(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, device: torch.device) -> int:
-    if t.dtype != dtype:
+def _dense(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, index: int) -> int:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {list(shape)} on the cache's device")
     return t.data_ptr()
 
 
-def _bytes(workspace: torch.Tensor | None, device: torch.device) -> tuple[int | None, int]:
+def _bytes(workspace: torch.Tensor | None, index: int) -> tuple[int | None, int]:
     if workspace is None:
         return None, 0
-    if workspace.device != device or not workspace.is_contiguous():
+    if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor | None:
     return new_workspace(nbytes, device) if nbytes else None
+
+
+def _heads(q: torch.Tensor, c: _Caches) -> None:
+    if q.shape[-1] != c.D:
+        raise ValueError("q and the cache have different head dims")
 
 
 # ------------------------------------------------------------------- rope --
@@ -83,11 +97,11 @@ def qsa_rope_freqs(rotary_dim: int, theta: float = 10000.0, scaling: str = "none
     return list(fr[:n]), list(inv[:n]), m.value
 
 
-def _rows(t: torch.Tensor, dtype, heads: int, D: int, n: int, name: str, device) -> tuple[int, int]:
+def _rows(t: torch.Tensor, dtype, heads: int, D: int, n: int, name: str, index: int) -> tuple[int, int]:
     """(pointer, row stride) of t [n, heads, D] whose rows are dense."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (n, heads, D) or t.device != device:
+    if t.shape != (n, heads, D) or t.get_device() != index:
         raise ValueError(f"{name} must be [{n}, {heads}, {D}] on the cache's device")
     s = t.stride()
     if (s[2] != 1 or (heads > 1 and s[1] != D)) and n > 0:
@@ -95,21 +109,15 @@ def _rows(t: torch.Tensor, dtype, heads: int, D: int, n: int, name: str, device)
     return t.data_ptr(), s[0] if n > 1 else heads * D
 
 
-def _rope_append(ref, cache, freqs, rotary_dim, interleaved, mscale, pos0, cu_new, q, k, v, q_out, stream):
-    kc = cache.k_cache
-    dev, (_, _, Hkv, D) = kc.device, kc.shape
-    dt = _query_type(cache)
-    n, Hq = q.shape[0], q.shape[1]
-    B = pos0.shape[0]
-    qp, qs = _rows(q, dt, Hq, D, n, "q", dev)
-    kp, ks = _rows(k, dt, Hkv, D, n, "k", dev)
-    vp, vs = _rows(v, dt, Hkv, D, n, "v", dev)
-    op = _dense(q_out, dt, (n, Hq, D), "q_out", dev)
-    args = (ref, B, n, _ints(pos0, B, "pos0", dev), _ints(cu_new, B + 1, "cu_new", dev), qp, qs, kp, ks, vp, vs,
-            _Q_DTYPES[dt], Hq, freqs.data_ptr() if rotary_dim else None, rotary_dim, 1 if interleaved else 0,
-            mscale, op)
-    with _device(dev.index):
-        _check(_lib.load().qsa_rope_append(*args, _stream(stream, dev.index)), "qsa_rope_append")
+def _rope_append(c: _Caches, fn, freqs, rotary_dim, layout, mscale, pos0, cu_new, q, k, v, q_out, stream):
+    n, Hq, _ = q.shape
+    B, dt, ix, D = pos0.shape[0], c.dtype, c.index, c.D
+    qp, qs = _rows(q, dt, Hq, D, n, "q", ix)
+    kp, ks = _rows(k, dt, c.Hkv, D, n, "k", ix)
+    vp, vs = _rows(v, dt, c.Hkv, D, n, "v", ix)
+    _call(fn, "qsa_rope_append", ix,
+          (c.ref, B, n, _ints(pos0, B, "pos0", ix), _ints(cu_new, B + 1, "cu_new", ix), qp, qs, kp, ks, vp, vs,
+           c.qd, Hq, freqs, rotary_dim, layout, mscale, _dense(q_out, dt, (n, Hq, D), "q_out", ix)), stream)
 
 
 def qsa_rope_append(cache: QSACache, pos0: torch.Tensor, cu_new: torch.Tensor, q: torch.Tensor,
@@ -120,12 +128,12 @@ def qsa_rope_append(cache: QSACache, pos0: torch.Tensor, cu_new: torch.Tensor, q
     device, the bits of qsa_rope_freqs.  q, k, v may be strided over tokens
     (parts of one fused projection)."""
     rotary_dim = int(rotary_dim)
+    c = _Caches(cache)
     _need(freqs, torch.int64, "freqs")
-    if freqs.shape != (max(rotary_dim, 0) // 2,) or freqs.device != cache.k_cache.device or not freqs.is_contiguous():
+    if freqs.shape != (max(rotary_dim, 0) // 2,) or freqs.get_device() != c.index or not freqs.is_contiguous():
         raise ValueError("freqs must hold rotary_dim / 2 entries on the cache's device")
-    s = cache.struct()
-    _rope_append(ctypes.byref(s), cache, freqs, rotary_dim, interleaved, float(mscale), pos0, cu_new, q, k, v,
-                 q_out, stream)
+    _rope_append(c, _lib.load().qsa_rope_append, freqs.data_ptr() if rotary_dim else None, rotary_dim,
+                 int(bool(interleaved)), float(mscale), pos0, cu_new, q, k, v, q_out, stream)
 
 
 class QSARopeAppend:
@@ -143,16 +151,15 @@ class QSARopeAppend:
                                                            original_max_position, beta_fast, beta_slow)
         self.freqs = torch.tensor([f - (1 << 64) if f >> 63 else f for f in turns], dtype=torch.int64,
                                   device=cache.k_cache.device)
-        self._struct = cache.struct()
-        self._ref = ctypes.byref(self._struct)
+        self._c, self._fn = _Caches(cache), _lib.load().qsa_rope_append
 
     def __call__(self, pos0, cu_new, q, k, v, q_out=None, stream=None) -> torch.Tensor:
         if q.dim() != 3 or q.shape[1] != self.Hq:
             raise ValueError(f"q must be [N, {self.Hq}, D]")
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _rope_append(self._ref, self.cache, self.freqs, self.rotary_dim, self.interleaved, self.mscale, pos0,
-                     cu_new, q, k, v, q_out, stream)
+        _rope_append(self._c, self._fn, self.freqs.data_ptr() if self.rotary_dim else None, self.rotary_dim,
+                     int(self.interleaved), self.mscale, pos0, cu_new, q, k, v, q_out, stream)
         return q_out
 
 
@@ -161,18 +168,12 @@ def qsa_window_decode_workspace_bytes(cache: QSACache, B: int, T: int, Hq: int, 
     return int(_lib.load().qsa_window_decode_workspace_bytes(ctypes.byref(cache.struct()), B, T, Hq, window, sinks))
 
 
-def _window_decode(ref, cache, q, ctx_lens, window, sinks, sm_scale, o, lse, workspace, stream):
-    kc = cache.k_cache
-    dev, dt = kc.device, _query_type(cache)
-    B, T, Hq, D = q.shape
-    if D != kc.shape[3]:
-        raise ValueError("q and the cache have different head dims")
-    wp, wn = _bytes(workspace, dev)
-    args = (ref, B, T, Hq, _dense(q, dt, (B, T, Hq, D), "q", dev), _Q_DTYPES[dt],
-            _ints(ctx_lens, B, "ctx_lens", dev), window, sinks, sm_scale, _dense(o, dt, (B, T, Hq, D), "o", dev),
-            _dense(lse, torch.float32, (B, T, Hq), "lse", dev), wp, wn)
-    with _device(dev.index):
-        _check(_lib.load().qsa_window_decode(*args, _stream(stream, dev.index)), "qsa_window_decode")
+def _window_decode(c: _Caches, fn, q, ctx_lens, window, sinks, sm_scale, o, lse, ws, stream):
+    B, T, Hq, D = shape = q.shape
+    dt, ix = c.dtype, c.index
+    _call(fn, "qsa_window_decode", ix,
+          (c.ref, B, T, Hq, _dense(q, dt, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix), window, sinks,
+           sm_scale, _dense(o, dt, shape, "o", ix), _dense(lse, torch.float32, shape[:3], "lse", ix), *ws), stream)
 
 
 def qsa_window_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, window: int, sinks: int,
@@ -180,9 +181,10 @@ def qsa_window_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
                       stream=None) -> None:
     """Decode attention of q [B, T, Hq, D] over each request's last `window`
     keys and first `sinks` keys.  o: q's type and shape, lse float32."""
-    s = cache.struct()
-    _window_decode(ctypes.byref(s), cache, q, ctx_lens, int(window), int(sinks), float(sm_scale), o, lse,
-                   workspace, stream)
+    c = _Caches(cache)
+    _heads(q, c)
+    _window_decode(c, _lib.load().qsa_window_decode, q, ctx_lens, int(window), int(sinks), float(sm_scale), o, lse,
+                   _bytes(workspace, c.index), stream)
 
 
 class QSAWindowDecode:
@@ -190,20 +192,19 @@ class QSAWindowDecode:
 
     def __init__(self, cache: QSACache, B: int, T: int, Hq: int, window: int, sinks: int = 0,
                  sm_scale: float | None = None):
-        dev, D = cache.k_cache.device, cache.k_cache.shape[-1]
         self.cache, self.window, self.sinks = cache, int(window), int(sinks)
-        self.sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-        self._struct = cache.struct()
-        self._ref = ctypes.byref(self._struct)
-        self.o = torch.empty((B, T, Hq, D), dtype=_query_type(cache), device=dev)
-        self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
-        self.ws = _workspace(qsa_window_decode_workspace_bytes(cache, B, T, Hq, self.window, self.sinks), dev)
+        c = self._c = _Caches(cache)
+        self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
+        self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)
+        self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=c.device)
+        self.ws = _workspace(qsa_window_decode_workspace_bytes(cache, B, T, Hq, self.window, self.sinks), c.device)
+        self._ws, self._fn = _bytes(self.ws, c.index), _lib.load().qsa_window_decode
 
     def __call__(self, q, ctx_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         if q.shape != self.o.shape:
             raise ValueError(f"q must be {list(self.o.shape)}")
-        _window_decode(self._ref, self.cache, q, ctx_lens, self.window, self.sinks, self.sm_scale, self.o,
-                       self.lse, self.ws, stream)
+        _window_decode(self._c, self._fn, q, ctx_lens, self.window, self.sinks, self.sm_scale, self.o, self.lse,
+                       self._ws, stream)
         return self.o, self.lse
 
 
@@ -213,19 +214,13 @@ def qsa_window_prefill_workspace_bytes(cache: QSACache, B: int, n_tokens: int, m
                                                               max_q_per_req, Hq, window, sinks))
 
 
-def _window_prefill(ref, cache, cu_q, ctx_lens, max_q_per_req, q, window, sinks, sm_scale, o, lse, workspace, stream):
-    kc = cache.k_cache
-    dev, dt = kc.device, _query_type(cache)
-    n, Hq, D = q.shape
-    if D != kc.shape[3]:
-        raise ValueError("q and the cache have different head dims")
-    B = ctx_lens.shape[0]
-    wp, wn = _bytes(workspace, dev)
-    args = (ref, B, n, max_q_per_req, _ints(cu_q, B + 1, "cu_q", dev), _ints(ctx_lens, B, "ctx_lens", dev),
-            _dense(q, dt, (n, Hq, D), "q", dev), _Q_DTYPES[dt], Hq, window, sinks, sm_scale,
-            _dense(o, dt, (n, Hq, D), "o", dev), _dense(lse, torch.float32, (n, Hq), "lse", dev), wp, wn)
-    with _device(dev.index):
-        _check(_lib.load().qsa_window_prefill(*args, _stream(stream, dev.index)), "qsa_window_prefill")
+def _window_prefill(c: _Caches, fn, cu_q, ctx_lens, max_q, q, window, sinks, sm_scale, o, lse, ws, stream):
+    n, Hq, D = shape = q.shape
+    B, dt, ix = ctx_lens.shape[0], c.dtype, c.index
+    _call(fn, "qsa_window_prefill", ix,
+          (c.ref, B, n, max_q, _ints(cu_q, B + 1, "cu_q", ix), _ints(ctx_lens, B, "ctx_lens", ix),
+           _dense(q, dt, shape, "q", ix), c.qd, Hq, window, sinks, sm_scale, _dense(o, dt, shape, "o", ix),
+           _dense(lse, torch.float32, shape[:2], "lse", ix), *ws), stream)
 
 
 def qsa_window_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tensor, max_q_per_req: int,
@@ -233,9 +228,10 @@ def qsa_window_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tens
                        lse: torch.Tensor, workspace: torch.Tensor | None, stream=None) -> None:
     """Window attention of a prefill chunk: rows cu_q[r] .. cu_q[r+1]-1 of q
     [N, Hq, D] are the newest tokens of request r."""
-    s = cache.struct()
-    _window_prefill(ctypes.byref(s), cache, cu_q, ctx_lens, int(max_q_per_req), q, int(window), int(sinks),
-                    float(sm_scale), o, lse, workspace, stream)
+    c = _Caches(cache)
+    _heads(q, c)
+    _window_prefill(c, _lib.load().qsa_window_prefill, cu_q, ctx_lens, int(max_q_per_req), q, int(window), int(sinks),
+                    float(sm_scale), o, lse, _bytes(workspace, c.index), stream)
 
 
 class QSAWindowPrefill:
@@ -243,22 +239,21 @@ class QSAWindowPrefill:
 
     def __init__(self, cache: QSACache, B: int, n_tokens: int, max_q_per_req: int, Hq: int, window: int,
                  sinks: int = 0, sm_scale: float | None = None):
-        dev, D = cache.k_cache.device, cache.k_cache.shape[-1]
         self.cache, self.window, self.sinks = cache, int(window), int(sinks)
         self.B, self.max_q = B, int(max_q_per_req)
-        self.sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-        self._struct = cache.struct()
-        self._ref = ctypes.byref(self._struct)
-        self.o = torch.zeros((n_tokens, Hq, D), dtype=_query_type(cache), device=dev)
-        self.lse = torch.full((n_tokens, Hq), -math.inf, dtype=torch.float32, device=dev)
+        c = self._c = _Caches(cache)
+        self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
+        self.o = torch.zeros((n_tokens, Hq, c.D), dtype=c.dtype, device=c.device)
+        self.lse = torch.full((n_tokens, Hq), -math.inf, dtype=torch.float32, device=c.device)
         self.ws = _workspace(qsa_window_prefill_workspace_bytes(cache, B, n_tokens, self.max_q, Hq, self.window,
-                                                                self.sinks), dev)
+                                                                self.sinks), c.device)
+        self._ws, self._fn = _bytes(self.ws, c.index), _lib.load().qsa_window_prefill
 
     def __call__(self, q, cu_q, ctx_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         if q.shape != self.o.shape or ctx_lens.shape != (self.B,):
             raise ValueError(f"q must be {list(self.o.shape)} and ctx_lens [{self.B}]")
-        _window_prefill(self._ref, self.cache, cu_q, ctx_lens, self.max_q, q, self.window, self.sinks,
-                        self.sm_scale, self.o, self.lse, self.ws, stream)
+        _window_prefill(self._c, self._fn, cu_q, ctx_lens, self.max_q, q, self.window, self.sinks, self.sm_scale,
+                        self.o, self.lse, self._ws, stream)
         return self.o, self.lse
 
 
@@ -269,21 +264,13 @@ def qsa_prefix_decode_workspace_bytes(cache: QSACache, B: int, T: int, Hq: int, 
                                                              max_group, max_prefix, max_tail))
 
 
-def _prefix_decode(ref, cache, q, ctx_lens, cu_group, prefix_lens, max_group, max_prefix, max_tail, sm_scale, o,
-                   lse, workspace, stream):
-    kc = cache.k_cache
-    dev, dt = kc.device, _query_type(cache)
-    B, T, Hq, D = q.shape
-    if D != kc.shape[3]:
-        raise ValueError("q and the cache have different head dims")
-    n = prefix_lens.shape[0]
-    wp, wn = _bytes(workspace, dev)
-    args = (ref, B, T, Hq, _dense(q, dt, (B, T, Hq, D), "q", dev), _Q_DTYPES[dt],
-            _ints(ctx_lens, B, "ctx_lens", dev), n, _ints(cu_group, n + 1, "cu_group", dev),
-            _ints(prefix_lens, n, "prefix_lens", dev), max_group, max_prefix, max_tail, sm_scale,
-            _dense(o, dt, (B, T, Hq, D), "o", dev), _dense(lse, torch.float32, (B, T, Hq), "lse", dev), wp, wn)
-    with _device(dev.index):
-        _check(_lib.load().qsa_prefix_decode(*args, _stream(stream, dev.index)), "qsa_prefix_decode")
+def _prefix_decode(c: _Caches, fn, q, ctx_lens, cu_group, prefix_lens, bounds, sm_scale, o, lse, ws, stream):
+    B, T, Hq, D = shape = q.shape
+    n, dt, ix = prefix_lens.shape[0], c.dtype, c.index
+    _call(fn, "qsa_prefix_decode", ix,
+          (c.ref, B, T, Hq, _dense(q, dt, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix), n,
+           _ints(cu_group, n + 1, "cu_group", ix), _ints(prefix_lens, n, "prefix_lens", ix), *bounds, sm_scale,
+           _dense(o, dt, shape, "o", ix), _dense(lse, torch.float32, shape[:3], "lse", ix), *ws), stream)
 
 
 def qsa_prefix_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, cu_group: torch.Tensor,
@@ -291,9 +278,11 @@ def qsa_prefix_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
                       o: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """Decode attention of q [B, T, Hq, D] where the requests of a group share
     their first prefix_lens[g] keys."""
-    s = cache.struct()
-    _prefix_decode(ctypes.byref(s), cache, q, ctx_lens, cu_group, prefix_lens, int(max_group), int(max_prefix),
-                   int(max_tail), float(sm_scale), o, lse, workspace, stream)
+    c = _Caches(cache)
+    _heads(q, c)
+    _prefix_decode(c, _lib.load().qsa_prefix_decode, q, ctx_lens, cu_group, prefix_lens,
+                   (int(max_group), int(max_prefix), int(max_tail)), float(sm_scale), o, lse,
+                   _bytes(workspace, c.index), stream)
 
 
 class QSAPrefixDecode:
@@ -301,19 +290,18 @@ class QSAPrefixDecode:
 
     def __init__(self, cache: QSACache, B: int, T: int, Hq: int, n_groups: int, max_group: int, max_prefix: int,
                  max_tail: int, sm_scale: float | None = None):
-        dev, D = cache.k_cache.device, cache.k_cache.shape[-1]
         self.cache, self.n_groups = cache, n_groups
         self.bounds = (int(max_group), int(max_prefix), int(max_tail))
-        self.sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-        self._struct = cache.struct()
-        self._ref = ctypes.byref(self._struct)
-        self.o = torch.empty((B, T, Hq, D), dtype=_query_type(cache), device=dev)
-        self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
-        self.ws = _workspace(qsa_prefix_decode_workspace_bytes(cache, B, T, Hq, n_groups, *self.bounds), dev)
+        c = self._c = _Caches(cache)
+        self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
+        self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)
+        self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=c.device)
+        self.ws = _workspace(qsa_prefix_decode_workspace_bytes(cache, B, T, Hq, n_groups, *self.bounds), c.device)
+        self._ws, self._fn = _bytes(self.ws, c.index), _lib.load().qsa_prefix_decode
 
     def __call__(self, q, ctx_lens, cu_group, prefix_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         if q.shape != self.o.shape or prefix_lens.shape != (self.n_groups,):
             raise ValueError(f"q must be {list(self.o.shape)} and prefix_lens [{self.n_groups}]")
-        _prefix_decode(self._ref, self.cache, q, ctx_lens, cu_group, prefix_lens, *self.bounds, self.sm_scale,
-                       self.o, self.lse, self.ws, stream)
+        _prefix_decode(self._c, self._fn, q, ctx_lens, cu_group, prefix_lens, self.bounds, self.sm_scale, self.o,
+                       self.lse, self._ws, stream)
         return self.o, self.lse

@@ -16,12 +16,15 @@ namespace {
 // Splits and workspace sizes are planned for this many SMs (B200), so that
 // they depend on the call's shape alone.
 constexpr int kPlanSMs = 148;
+constexpr int kMaxCluster = 8;  // portable cluster size
 
 // ------------------------------------------------------------------ plan --
 // How one launch covers the keys of its rows: `splits` slots each.
 struct AttnPlan {
   int splits;       // of this launch
   long long tiles;  // row tiles of a sequence
+  bool cluster;     // the splits merge within the launch: no slots
+  int slots() const { return cluster ? 1 : splits; }
 };
 
 long long ceil_ll(long long a, long long b) { return (a + b - 1) / b; }
@@ -32,7 +35,7 @@ long long span_bound(long long window, long long sinks, long long tokens, long l
 }
 
 AttnPlan plan_simple(long long seqs, int Hkv, long long rows, long long span) {
-  AttnPlan p;
+  AttnPlan p = {};
   p.tiles = ceil_ll(std::max(rows, 1LL), qsa::attn::kSimpleRows);
   const long long ctas = std::max(1LL, seqs * Hkv * p.tiles);
   p.splits = (int)std::max(1LL, std::min({4LL * kPlanSMs / ctas, ceil_ll(span, 2 * qsa::attn::kSimpleKeys), 64LL}));
@@ -40,19 +43,28 @@ AttnPlan plan_simple(long long seqs, int Hkv, long long rows, long long span) {
 }
 
 // Few rows of a 16-bit or 8-bit cache: one CTA of the streaming kernel per
-// (request, kv head, split).
-AttnPlan plan_stream(long long seqs, int Hkv, long long span) {
-  AttnPlan p;
+// (request, kv head, split).  `merge`: the splits are all there is to a row.
+AttnPlan plan_stream(long long seqs, int Hkv, long long span, bool merge) {
+  AttnPlan p = {};
   p.tiles = 1;
   const long long pairs = std::max(1LL, seqs * Hkv);
-  p.splits = (int)std::max(1LL, std::min({4LL * kPlanSMs / pairs, ceil_ll(span, 256), 64LL}));
+  if (merge) {
+    // two CTAs an SM; up to 8 of a row form a cluster, also where there is
+    // room for more, up to 1,024 keys each
+    p.splits = (int)std::max(1LL, std::min({2LL * kPlanSMs / pairs, ceil_ll(span, 128), 64LL}));
+    if (p.splits > kMaxCluster && span <= 1024LL * kMaxCluster) p.splits = kMaxCluster;
+    p.cluster = p.splits > 1 && p.splits <= kMaxCluster;
+  } else {
+    // tails of very different lengths: more and smaller pieces
+    p.splits = (int)std::max(1LL, std::min({8LL * kPlanSMs / pairs, ceil_ll(span, 256), 64LL}));
+  }
   return p;
 }
 
 // Many rows of a 16-bit or 8-bit cache: one CTA (an SM's) of the tensor-core
 // kernel per (sequence, kv head, 256 rows, split).
 AttnPlan plan_tiles(long long seqs, int Hkv, long long rows, long long span) {
-  AttnPlan p;
+  AttnPlan p = {};
   p.tiles = ceil_ll(std::max(rows, 1LL), 2 * qsa::attn::kTileRows);
   const long long ctas = std::max(1LL, seqs * Hkv * p.tiles);
   p.splits = (int)std::max(1LL, std::min({kPlanSMs / ctas, ceil_ll(span, 4 * qsa::attn::kTileKeys), 64LL}));
@@ -202,8 +214,8 @@ qsa_status launch_stream(const qsa::attn::Args &a, const AttnPlan &pl, cudaStrea
     std::lock_guard<std::mutex> lk(g_mutex);
     if (prepare_kernel(kernel, smem, done) != cudaSuccess) return QSA_ERR_CUDA;
   }
-  return launch(true, kernel, dim3((unsigned)pl.splits, (unsigned)a.c.num_kv_heads, (unsigned)a.B),
-                dim3(qsa::attn::kDecThreads), smem, s, a);
+  return launch_cluster(true, kernel, dim3((unsigned)pl.splits, (unsigned)a.c.num_kv_heads, (unsigned)a.B),
+                dim3(qsa::attn::kDecThreads), smem, s, pl.cluster ? pl.splits : 1, a);
 }
 
 template <int MODE, int D, bool FP8>
@@ -220,6 +232,7 @@ qsa_status launch_decode_rows(qsa::attn::Args a, const AttnPlan &pl, int slot0, 
   if (a.c.kv_dtype == QSA_F32) return launch_rows<MODE>(a, pl, a.B, slot0, s);
   a.slot0 = slot0;
   a.splits = pl.splits;
+  a.cluster = pl.cluster;
   if (a.c.num_kv_heads > 65535) return QSA_ERR_UNSUPPORTED;
   const bool fp8 = a.c.kv_dtype == QSA_FP8_E4M3;
   if (a.c.head_dim == 64)
@@ -243,9 +256,9 @@ qsa_status launch_attn_merge(const qsa::attn::Args &a, cudaStream_t s) {
                                          : launch_attn_merge_w<qsa::attn::kMergeWarps>(a, s);
 }
 
-AttnPlan plan_decode(const qsa_cache *c, int B, int T, int Hq, long long window, long long sinks) {
+AttnPlan plan_decode(const qsa_cache *c, int B, int T, int Hq, long long window, long long sinks, bool merge) {
   const long long span = span_bound(window, sinks, T, ctx_cap(c));
-  if (c->kv_dtype != QSA_F32) return plan_stream(B, c->num_kv_heads, span);
+  if (c->kv_dtype != QSA_F32) return plan_stream(B, c->num_kv_heads, span, merge);
   return plan_simple(B, c->num_kv_heads, (long long)T * (Hq / c->num_kv_heads), span);
 }
 
@@ -401,7 +414,7 @@ size_t qsa_window_decode_workspace_bytes(const qsa_cache *cache, int32_t B, int3
   if (check_cache(cache) != QSA_OK || B < 1 || T < 1 || Hq < 1 || Hq % cache->num_kv_heads != 0 || window < 1 ||
       sinks < 0)
     return 0;
-  return parts_bytes((long long)B * T * Hq, plan_decode(cache, B, T, Hq, window, sinks).splits, cache->head_dim);
+  return parts_bytes((long long)B * T * Hq, plan_decode(cache, B, T, Hq, window, sinks, true).slots(), cache->head_dim);
 }
 
 qsa_status qsa_window_decode(const qsa_cache *cache, int32_t B, int32_t T, int32_t Hq, const void *q, int32_t q_dtype,
@@ -415,14 +428,14 @@ qsa_status qsa_window_decode(const qsa_cache *cache, int32_t B, int32_t T, int32
   if (!q || !ctx_lens || !o || !lse || !aligned(q, 16) || !aligned(o, 16)) return QSA_ERR_INVALID_ARG;
   const size_t need = qsa_window_decode_workspace_bytes(cache, B, T, Hq, window, sinks);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return QSA_ERR_INVALID_ARG;
-  const AttnPlan pl = plan_decode(cache, B, T, Hq, window, sinks);
+  const AttnPlan pl = plan_decode(cache, B, T, Hq, window, sinks, true);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   qsa::attn::Args a = attn_args(cache, B, T, Hq, B * T, q, ctx_lens, sm_scale, o, lse);
   a.window = window;
   a.sinks = sinks;
-  set_parts(a, pl.splits, workspace);
+  set_parts(a, pl.slots(), workspace);
   st = launch_decode_rows<qsa::attn::kWindow>(a, pl, 0, s);
-  return st != QSA_OK || pl.splits == 1 ? st : launch_attn_merge(a, s);
+  return st != QSA_OK || pl.slots() == 1 ? st : launch_attn_merge(a, s);
 }
 
 size_t qsa_window_prefill_workspace_bytes(const qsa_cache *cache, int32_t B, int32_t n_tokens, int32_t max_q_per_req,
@@ -465,7 +478,7 @@ size_t qsa_prefix_decode_workspace_bytes(const qsa_cache *cache, int32_t B, int3
       !prefix_args_ok(B, n_groups, max_group, max_prefix, max_tail))
     return 0;
   const int slots = plan_shared(cache, n_groups, max_group, T, Hq, max_prefix).splits +
-                    plan_decode(cache, B, T, Hq, std::max(max_tail, 1), 0).splits;
+                    plan_decode(cache, B, T, Hq, std::max(max_tail, 1), 0, false).splits;
   return parts_bytes((long long)B * T * Hq, slots, cache->head_dim);
 }
 
@@ -485,7 +498,7 @@ qsa_status qsa_prefix_decode(const qsa_cache *cache, int32_t B, int32_t T, int32
   const size_t need = qsa_prefix_decode_workspace_bytes(cache, B, T, Hq, n_groups, max_group, max_prefix, max_tail);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return QSA_ERR_INVALID_ARG;
   const AttnPlan shared = plan_shared(cache, n_groups, max_group, T, Hq, max_prefix);
-  const AttnPlan tail = plan_decode(cache, B, T, Hq, std::max(max_tail, 1), 0);
+  const AttnPlan tail = plan_decode(cache, B, T, Hq, std::max(max_tail, 1), 0, false);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   qsa::attn::Args a = attn_args(cache, B, T, Hq, B * T, q, ctx_lens, sm_scale, o, lse);
   a.cu = cu_group;

@@ -55,6 +55,7 @@ struct Args {
   int slots;        // 1: the kernel writes o / lse itself
   int slot0;        // first slot of this launch
   int splits;       // slots of this launch
+  int cluster;      // the splits of a row are the CTAs of a cluster, which merge among themselves
 };
 
 // One sequence of query tokens.

@@ -8,7 +8,11 @@
 // takes a split of one (request, kv head); each warp streams a contiguous part
 // of it, 16 keys a stage, through its own cp.async ring with its own running
 // maximum and sum (no barriers while it streams), and the four results are
-// merged in shared memory.  fp8 tiles go from shared memory into f16 fragments
+// merged in shared memory.  The splits of a (request, kv head), up to 8, are a
+// cluster that merges its results through distributed shared memory (a merge
+// kernel behind it cost 4 us a call and the partial results' way to memory);
+// only more splits, and tails, whose prefix part comes from another kernel, go
+// through the workspace.  fp8 tiles go from shared memory into f16 fragments
 // (fp8_frag.cuh).
 //
 // Weights p = exp(s - max) enter the value product rounded to bf16 (2^-9
@@ -45,7 +49,36 @@ struct DecSmem {
     float o[kDecWarps][NT * 8][D];
   };
   float m[kDecWarps][NT * 8], l[kDecWarps][NT * 8];
+  float cm[NT * 8], cl[NT * 8];  // the CTA's: maximum and sum (its values: o[0])
+  // more than 16 rows: their Q fragments (64 registers at 32 rows), by tile,
+  // k-step and lane, and the rows' factor on the logits
+  uint2 qf[NT > 2 ? NT : 1][NT > 2 ? D / 16 : 1][32];
+  float qs[NT * 8];
 };
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word or four words at `p` of this CTA's shared memory, in CTA `rank` of
+// the cluster.
+__device__ __forceinline__ uint32_t peer_at(const void *p, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float peer_float(const float *p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_at(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_float4(const float *p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_at(p, rank))
+               : "memory");
+  return v;
+}
 
 // Grid (splits, Hkv, requests).
 template <int MODE, int D, bool FP8, int NT>
@@ -82,6 +115,36 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
     lcol[j][0] = lcol[j][1] = 0.f;
   }
   float vsref = 0.f;  // power of two that the V scales are relative to
+
+  // fragments of rows 8 j .. 8 j + 7; returns row 8 j + gq's factor on the logits
+  auto q_frags = [&](int j, uint32_t(&f)[MD][2]) -> float {
+    const int m = 8 * j + gq;
+    const __nv_bfloat16 *qrow =
+        m < M ? static_cast<const __nv_bfloat16 *>(a.q) +
+                    ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D
+              : nullptr;
+    if constexpr (FP8) {
+      return q_frags_f16<D>(qrow, cq, f) * a.scale_log2;
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < MD; ++kk) {
+        f[kk][0] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq) : 0u;
+        f[kk][1] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq + 8) : 0u;
+      }
+      return a.scale_log2;
+    }
+  };
+  constexpr bool kQRegs = NT <= 2;
+  if constexpr (!kQRegs) {
+    if (warp < NT) {
+      uint32_t f[MD][2];
+      const float sc = q_frags(warp, f);
+#pragma unroll
+      for (int kk = 0; kk < MD; ++kk) sm.qf[warp][kk][lane] = make_uint2(f[kk][0], f[kk][1]);
+      if (cq == 0) sm.qs[8 * warp + gq] = sc;
+    }
+    __syncthreads();
+  }
 
   // this warp's part of the split
   const int w0 = x0 + split_bound(x1 - x0, kDecWarps, warp, kStageKeys);
@@ -144,27 +207,19 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
       cp_async_commit();
     }
     // ---- Q as B fragments, rows past M zero
-    uint32_t qb[NT][MD][2];
+    uint32_t qb[kQRegs ? NT : 1][MD][2];
     float csc[NT][2];
     int rlo[NT][2], rhi[NT][2], rsink = MODE == kWindow ? a.sinks : 0;
     int all_lo = 0, all_hi = 0x7fffffff;  // keys in [all_lo, all_hi) are seen by every row
-    const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(a.q);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int m = 8 * j + gq;
-      const __nv_bfloat16 *qrow =
-          m < M ? qg + ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D : nullptr;
-      if constexpr (FP8) {
-        const float sc = q_frags_f16<D>(qrow, cq, qb[j]);
-        csc[j][0] = __shfl_sync(0xffffffffu, sc, 4 * (2 * cq)) * a.scale_log2;
-        csc[j][1] = __shfl_sync(0xffffffffu, sc, 4 * (2 * cq + 1)) * a.scale_log2;
+      if constexpr (kQRegs) {
+        const float sc = q_frags(j, qb[j]);
+        csc[j][0] = __shfl_sync(0xffffffffu, sc, 4 * (2 * cq));
+        csc[j][1] = __shfl_sync(0xffffffffu, sc, 4 * (2 * cq + 1));
       } else {
-#pragma unroll
-        for (int kk = 0; kk < MD; ++kk) {
-          qb[j][kk][0] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq) : 0u;
-          qb[j][kk][1] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq + 8) : 0u;
-        }
-        csc[j][0] = csc[j][1] = a.scale_log2;
+        csc[j][0] = sm.qs[8 * j + 2 * cq];
+        csc[j][1] = sm.qs[8 * j + 2 * cq + 1];
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -225,7 +280,20 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
         for (int e = 0; e < 4; ++e) sacc[j][e] = sac2[j][e] = 0.f;
       if constexpr (FP8) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) qk_fp8<D>(kt, gq, cq, qb[j], sacc[j], sac2[j]);
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (kQRegs) {
+            qk_fp8<D>(kt, gq, cq, qb[j], sacc[j], sac2[j]);
+          } else {
+            uint32_t f[MD][2];
+#pragma unroll
+            for (int kk = 0; kk < MD; ++kk) {
+              const uint2 w = sm.qf[j][kk][lane];
+              f[kk][0] = w.x;
+              f[kk][1] = w.y;
+            }
+            qk_fp8<D>(kt, gq, cq, f, sacc[j], sac2[j]);
+          }
+        }
       } else {
 #pragma unroll
         for (int kk = 0; kk < MD; ++kk) {
@@ -233,8 +301,11 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
           ldsm_x4(a0, a1, a2, a3, kt + swz<D>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * kk + (lane >> 4)));
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            if (kk & 1) mma_bf16(sac2[j], a0, a1, a2, a3, qb[j][kk][0], qb[j][kk][1]);
-            else mma_bf16(sacc[j], a0, a1, a2, a3, qb[j][kk][0], qb[j][kk][1]);
+            uint2 w;
+            if constexpr (kQRegs) w = make_uint2(qb[j][kk][0], qb[j][kk][1]);
+            else w = sm.qf[j][kk][lane];
+            if (kk & 1) mma_bf16(sac2[j], a0, a1, a2, a3, w.x, w.y);
+            else mma_bf16(sacc[j], a0, a1, a2, a3, w.x, w.y);
           }
         }
       }
@@ -375,6 +446,7 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, sm.m[w][m]);
+    const float top = mx;
     if (mx == -INFINITY) mx = 0.f;
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -387,6 +459,14 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
       acc.y += f * v.y;
       acc.z += f * v.z;
       acc.w += f * v.w;
+    }
+    if (a.cluster) {
+      *reinterpret_cast<float4 *>(&sm.o[0][m][d]) = acc;  // (read by this thread alone)
+      if (d == 0) {
+        sm.cm[m] = top;
+        sm.cl[m] = l;
+      }
+      continue;
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN sum stays one)
     acc.x *= inv;
@@ -407,6 +487,36 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
       store4(static_cast<__nv_bfloat16 *>(a.o) + at * D + d, acc);
       if (d == 0) a.lse[at] = lse;
     }
+  }
+  if (a.cluster) {
+    cluster_sync_all();  // every CTA's results stand
+    for (int e = threadIdx.x + split * kDecThreads; e < M * kVec; e += kDecThreads * a.splits) {
+      const int m = e / kVec, d = e % kVec * 4;
+      float mx = -INFINITY;
+      for (int c = 0; c < a.splits; ++c) mx = fmaxf(mx, peer_float(&sm.cm[m], c));
+      if (mx == -INFINITY) mx = 0.f;
+      float l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = 0; c < a.splits; ++c) {
+        const float f = attn::ex2(peer_float(&sm.cm[m], c) - mx);
+        const float4 v = peer_float4(&sm.o[0][m][d], c);
+        l += f * peer_float(&sm.cl[m], c);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;  // (a NaN sum stays one)
+      acc.x *= inv;
+      acc.y *= inv;
+      acc.z *= inv;
+      acc.w *= inv;
+      const long long at = (long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G;
+      store4(static_cast<__nv_bfloat16 *>(a.o) + at * D + d, acc);
+      if (d == 0) a.lse[at] = l != 0.f ? (mx + __log2f(l)) * attn::kLn2 : -INFINITY;
+    }
+    cluster_sync_all();  // until every peer has read
   }
 }
 

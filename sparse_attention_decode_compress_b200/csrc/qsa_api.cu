@@ -56,25 +56,33 @@ qsa_status launch_status() {
 // persistent scan into the tail of the previous step's merge, and steps
 // measured ~12% slower on B200.  (Launched early with only the wait, so
 // that the scan follows it only when it ends, the 256k step still measured
-// ~2 us slower.)
+// ~2 us slower.)  `cluster`: CTAs of a thread-block cluster along x.
 template <typename... KArgs, typename... Args>
-qsa_status launch(bool programmatic, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                  cudaStream_t s, Args... args) {
-  cudaLaunchAttribute attr[1];
+qsa_status launch_cluster(bool programmatic, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t s, int cluster, Args... args) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = programmatic ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) != cudaSuccess) {
     cudaGetLastError();
     return QSA_ERR_CUDA;
   }
   return launch_status();
+}
+template <typename... KArgs, typename... Args>
+qsa_status launch(bool programmatic, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                  cudaStream_t s, Args... args) {
+  return launch_cluster(programmatic, kernel, grid, block, smem, s, 1, args...);
 }
 
 qsa_status check_cache(const qsa_cache *c) {
