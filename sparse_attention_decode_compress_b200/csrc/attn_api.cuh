@@ -67,7 +67,10 @@ AttnPlan plan_tiles(long long seqs, int Hkv, long long rows, long long span) {
   AttnPlan p = {};
   p.tiles = ceil_ll(std::max(rows, 1LL), 2 * qsa::attn::kTileRows);
   const long long ctas = std::max(1LL, seqs * Hkv * p.tiles);
-  p.splits = (int)std::max(1LL, std::min({kPlanSMs / ctas, ceil_ll(span, 4 * qsa::attn::kTileKeys), 64LL}));
+  // one wave while that leaves a split 16 tiles of keys; otherwise about two,
+  // so that sequences of different lengths even out
+  const long long waves = seqs > 1 && ctas < kPlanSMs ? 2 : 1;
+  p.splits = (int)std::max(1LL, std::min({waves * kPlanSMs / ctas, ceil_ll(span, 4 * qsa::attn::kTileKeys), 64LL}));
   return p;
 }
 

@@ -147,6 +147,29 @@ __device__ __forceinline__ bool sees(const Seen &v, int key) {
   return key < v.hi && (key >= v.lo || key < v.sink);
 }
 
+// Programmatic launch of the three kernels of qsa_prefix_decode.  The tails'
+// kernel reads nothing that the prefixes' kernel writes, so it starts while that
+// one still runs, filling the SMs that run out of prefix work: the prefixes'
+// kernel lets it go only behind its own wait (what came before on the stream is
+// then complete for both), and the tails' kernel waits for it at its end, so that
+// the merge, which waits for the tails, waits for both.
+template <int MODE>
+__device__ __forceinline__ void pdl_begin() {
+  if (MODE == kShared) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (MODE == kWindow) {
+    pdl_open();
+  }
+}
+template <int MODE>
+__device__ __forceinline__ void pdl_end() {
+  if (MODE == kTail) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
+}
+
 // The keys that some token of [i0, i1) of the sequence may see, as a virtual
 // range: virtual key x is key x below sa, else b0 + x - sa.
 struct Range {

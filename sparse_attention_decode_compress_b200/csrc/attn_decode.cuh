@@ -83,7 +83,7 @@ __device__ __forceinline__ float4 peer_float4(const float *p, int rank) {
 // Grid (splits, Hkv, requests).
 template <int MODE, int D, bool FP8, int NT>
 __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Args a) {
-  pdl_open();
+  pdl_begin<MODE>();
   using namespace qsa::dec;
   constexpr int NS = dec_stages<FP8>();
   constexpr int MD = D / 16;
@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
     }
     cluster_sync_all();  // until every peer has read
   }
+  pdl_end<MODE>();
 }
 
 }  // namespace attn

@@ -31,7 +31,7 @@ __device__ __forceinline__ float4 load4(const void *p, long long at) {
 // Grid (row tiles, Hkv * splits, sequences).
 template <int MODE, int D>
 __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
-  pdl_open();
+  pdl_begin<MODE>();
   constexpr int kVec = D / 4;
   constexpr int kRowsPerWarp = kSimpleRows / 4;
   constexpr int kDims = D / 32;
@@ -41,7 +41,10 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
   const Seq sq = sequence<MODE>(a, blockIdx.z);
   const int m0 = blockIdx.x * kSimpleRows;
   const int rows = min(kSimpleRows, sq.ntok * a.G - m0);
-  if (rows <= 0) return;
+  if (rows <= 0) {
+    pdl_end<MODE>();
+    return;
+  }
   const int g = blockIdx.y / a.splits, split = blockIdx.y - g * a.splits;
   const Range rg = range_of<MODE>(a, sq, m0 / a.G, (m0 + rows - 1) / a.G + 1);
   const int x0 = split_bound(rg.n, a.splits, split, kSimpleKeys);
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
         static_cast<float *>(a.o)[at * D + lane + 32 * i] = o[j][i] * inv;
     }
   }
+  pdl_end<MODE>();
 }
 
 }  // namespace attn

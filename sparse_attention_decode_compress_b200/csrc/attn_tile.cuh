@@ -401,7 +401,7 @@ struct TileMaps {
 // Grid (row tiles of 256, Hkv * splits, sequences).
 template <int MODE, int D, bool FP8>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, const __grid_constant__ TileMaps maps) {
-  pdl_open();
+  pdl_begin<MODE>();
   using SM = TileSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   SM &sm = *reinterpret_cast<SM *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
