@@ -59,9 +59,9 @@ struct TileSmem {
   static constexpr int kTile = kTileKeys * D * 2;  // bytes of a key, value or query tile
   uint8_t q[2][kTile];
   uint8_t ring[kTileSlots][kTile];
-  // fp8: scales of a tile's keys and values, the largest |value scale| of each
+  // fp8: scales of a tile's keys and values by groups of four, the largest |value scale| of each
   // loader's share, and 2^-e of each query row (the row is scaled by 2^e)
-  float kscale[4][kTileKeys], vscale[4][kTileKeys], vmax[4][kTileLoaders], qscale[2 * kTileRows];
+  alignas(16) float kscale[4][kTileKeys / 4], vscale[4][kTileKeys / 4], vmax[4][kTileLoaders], qscale[2 * kTileRows];
   alignas(8) uint64_t full[kTileSlots], empty[kTileSlots];
   uint64_t qfull, sfull[2], pfull[2], ofull[2];
   uint32_t tmem;
@@ -289,12 +289,17 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first
   auto scores = [&](int c, uint32_t(&s)[32]) {
     if (FP8) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 k = *reinterpret_cast<const float4 *>(ksc + c + e);
-        s[e] = __float_as_uint(__uint_as_float(s[e]) * k.x);
-        s[e + 1] = __float_as_uint(__uint_as_float(s[e + 1]) * k.y);
-        s[e + 2] = __float_as_uint(__uint_as_float(s[e + 2]) * k.z);
-        s[e + 3] = __float_as_uint(__uint_as_float(s[e + 3]) * k.w);
+      for (int e = 0; e < 32; e += 16) {
+        const float4 k = *reinterpret_cast<const float4 *>(ksc + (c + e) / 4);
+        const float ks[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          float a, b;
+          unpack2(mul2(pack2(__uint_as_float(s[e + i]), __uint_as_float(s[e + i + 1])), pack2(ks[i / 4], ks[i / 4])),
+                  a, b);
+          s[e + i] = __float_as_uint(a);
+          s[e + i + 1] = __float_as_uint(b);
+        }
       }
     }
     if (MASKED) {
@@ -334,11 +339,9 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first
       sum0 = add2(sum0, pack2(x0, x1));
       sum1 = add2(sum1, pack2(x2, x3));
       if (FP8) {
-        const float4 v = *reinterpret_cast<const float4 *>(vsc + c + e);
-        x0 *= v.x * vinv;
-        x1 *= v.y * vinv;
-        x2 *= v.z * vinv;
-        x3 *= v.w * vinv;
+        const float v = vsc[(c + e) / 4] * vinv;
+        unpack2(mul2(pack2(x0, x1), pack2(v, v)), x0, x1);
+        unpack2(mul2(pack2(x2, x3), pack2(v, v)), x2, x3);
       }
       p[e / 2] = pack16<!FP8>(x0, x1);
       p[e / 2 + 1] = pack16<!FP8>(x2, x3);
@@ -788,6 +791,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
         }
       };
       if (nt > 0) fetch(0, raw[0]);
+      // the 32 bytes of a load are two chunks; half of the lanes write the second
+      // one first, so that the rows' halves, a column block apart, miss each
+      // other's banks
+      const int odd = ch >= kChunks / 2 ? 1 : 0;
       for (int j = 0; j < nt && ok; ++j) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -805,24 +812,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
+          uint8_t *tile = sm.ring[slot];
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
-            const int r = i * kRowsPer + lr;
+            const int r = wl * kRowsWarp + i * kRowsPer + lr;
             const uint4 x = raw[kv][i];
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t b[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              b[2 * k] = dec::e4m3x2_f16x2(w[k]);
-              b[2 * k + 1] = dec::e4m3x2_f16x2_hi(w[k]);
-            }
-            uint8_t *tile = sm.ring[slot];
-            *reinterpret_cast<uint4 *>(tile + tile_off(wl * kRowsWarp + r, 2 * ch)) = make_uint4(b[0], b[1], b[2], b[3]);
-            *reinterpret_cast<uint4 *>(tile + tile_off(wl * kRowsWarp + r, 2 * ch + 1)) = make_uint4(b[4], b[5], b[6], b[7]);
+            const uint4 lo = make_uint4(dec::e4m3x2_f16x2(x.x), dec::e4m3x2_f16x2_hi(x.x), dec::e4m3x2_f16x2(x.y),
+                                        dec::e4m3x2_f16x2_hi(x.y));
+            const uint4 hi = make_uint4(dec::e4m3x2_f16x2(x.z), dec::e4m3x2_f16x2_hi(x.z), dec::e4m3x2_f16x2(x.w),
+                                        dec::e4m3x2_f16x2_hi(x.w));
+            *reinterpret_cast<uint4 *>(tile + tile_off(r, 2 * ch + odd)) = odd ? hi : lo;
+            *reinterpret_cast<uint4 *>(tile + tile_off(r, 2 * ch + (odd ^ 1))) = odd ? lo : hi;
           }
           if (kv == 0) {  // (the softmax reads both behind the scores of this step)
-            sm.kscale[j & 3][wl * kRowsWarp + lane] = __shfl_sync(0xffffffffu, ks_now, lane >> 2);
-            sm.vscale[j & 3][wl * kRowsWarp + lane] = __shfl_sync(0xffffffffu, vs_now, lane >> 2);
+            if (lane < kRowsWarp / 4) {
+              sm.kscale[j & 3][wl * kRowsWarp / 4 + lane] = ks_now;
+              sm.vscale[j & 3][wl * kRowsWarp / 4 + lane] = vs_now;
+            }
             float v = fabsf(vs_now);
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
