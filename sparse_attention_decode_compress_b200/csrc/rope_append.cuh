@@ -118,9 +118,8 @@ __device__ __forceinline__ void st1(__nv_fp8_e4m3 *p, float x, float scale) {
 }
 
 // Where the K/V row of a token goes: cache row (of Hkv heads), or -1.
-__device__ __forceinline__ long long cache_row(const Params &p, int r, int tok, int &page) {
-  const long long pos = (long long)p.pos0[r] + (tok - p.cu[r]);
-  const long long lp = pos < 0 ? -1 : pos / p.c.page_size;
+__device__ __forceinline__ long long cache_row(const Params &p, long long pos, int r, int &page) {
+  const long long lp = pos < 0 ? -1 : pos <= 0x7fffffff ? (int)pos / p.c.page_size : pos / p.c.page_size;
   page = physical_page(p.c, r, lp);
   return page < 0 ? -1 : (long long)page * p.c.page_size + (pos - lp * p.c.page_size);
 }
@@ -161,16 +160,19 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(Params p) {
       x[j][1] = ld8(src + 8 * c1);
     }
   }
+  // lane i: pairs 2i and 2i + 1
+  uint64_t fr[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (2 * lane + e < p.R / 2) fr[e] = p.freqs[2 * lane + e];
   const int r = request_of(p.cu, p.B, tok, lane);
   if (r < 0) return;  // a row behind the last request
   const long long pos = (long long)p.pos0[r] + (tok - p.cu[r]);
   int page;
-  const long long row = cache_row(p, r, tok, page);
-  // lane i: pairs 2i and 2i + 1
-  float sn[2] = {0.f, 0.f}, cs[2] = {1.f, 1.f};
+  const long long row = cache_row(p, pos, r, page);
+  float sn[2], cs[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (2 * lane + e < p.R / 2) sincos_turns((uint64_t)pos * p.freqs[2 * lane + e], p.mscale, sn[e], cs[e]);
+  for (int e = 0; e < 2; ++e) sincos_turns((uint64_t)pos * fr[e], p.mscale, sn[e], cs[e]);
   float s8[8], c8[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(Params p, int
   if (r < 0) return;
   const long long pos = (long long)p.pos0[r] + (tok - p.cu[r]);
   int page;
-  const long long row = cache_row(p, r, tok, page);
+  const long long row = cache_row(p, pos, r, page);
   const int Hk = p.c.num_kv_heads, heads = p.Hq + 2 * Hk, half = p.R / 2;
   for (int e = lane; e < half + (D - p.R); e += 32) {
     const bool pair = e < half;
