@@ -564,6 +564,8 @@ qsa_status qsa_rope_append(const qsa_cache *cache, int32_t B, int32_t n_tokens, 
  *            is read, not its pointers)
  * Errors: QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED (types, head shapes, B
  * above 65535).
+ * One launch for up to 8 splits of a request's keys (a thread-block cluster),
+ * else a second one that merges them.
  */
 size_t qsa_window_decode_workspace_bytes(const qsa_cache *cache, int32_t B, int32_t T, int32_t Hq,
                                          int32_t window, int32_t sinks);
@@ -583,6 +585,8 @@ qsa_status qsa_window_decode(const qsa_cache *cache, int32_t B, int32_t T, int32
  *                  (QSA_ERR_BAD_INPUT on the device)
  *   q [n_tokens, Hq, D], o alike, lse [n_tokens, Hq]; Hq / Hkv <= 32
  *   the others as qsa_window_decode
+ * BF16 and FP8 caches run on the tensor cores (tcgen05); QSA_ERR_TIMEOUT on the
+ * device when one of its bounded waits ran out.
  */
 size_t qsa_window_prefill_workspace_bytes(const qsa_cache *cache, int32_t B, int32_t n_tokens,
                                           int32_t max_q_per_req, int32_t Hq, int32_t window,
@@ -599,7 +603,7 @@ qsa_status qsa_window_prefill(const qsa_cache *cache, int32_t B, int32_t n_token
  *
  * Requests cu_group[g] .. cu_group[g+1]-1 form group g; their first
  * prefix_lens[g] keys are the same, and are read through the block-table row
- * of the group's first request.  Keys from prefix_lens[g] on are each
+ * of the group's first request (which has to map all of them).  Keys from prefix_lens[g] on are each
  * request's own.  Query token t of request r sees every key i <=
  * ctx_lens[r] - T + t (a prefix longer than that is cut for it).  The prefix
  * and the tail are two partial results merged by log-sum-exp, as the KV

@@ -71,6 +71,13 @@ def _bytes(workspace: torch.Tensor | None, index: int) -> tuple[int | None, int]
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _int32(v, name: str) -> int:
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return v
+
+
 def _workspace(nbytes: int, device) -> torch.Tensor | None:
     return new_workspace(nbytes, device) if nbytes else None
 
@@ -183,8 +190,8 @@ def qsa_window_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
     keys and first `sinks` keys.  o: q's type and shape, lse float32."""
     c = _Caches(cache)
     _heads(q, c)
-    _window_decode(c, _lib.load().qsa_window_decode, q, ctx_lens, int(window), int(sinks), float(sm_scale), o, lse,
-                   _bytes(workspace, c.index), stream)
+    _window_decode(c, _lib.load().qsa_window_decode, q, ctx_lens, _int32(window, "window"), _int32(sinks, "sinks"),
+                   float(sm_scale), o, lse, _bytes(workspace, c.index), stream)
 
 
 class QSAWindowDecode:
@@ -192,7 +199,7 @@ class QSAWindowDecode:
 
     def __init__(self, cache: QSACache, B: int, T: int, Hq: int, window: int, sinks: int = 0,
                  sm_scale: float | None = None):
-        self.cache, self.window, self.sinks = cache, int(window), int(sinks)
+        self.cache, self.window, self.sinks = cache, _int32(window, "window"), _int32(sinks, "sinks")
         c = self._c = _Caches(cache)
         self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
         self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)
@@ -230,8 +237,9 @@ def qsa_window_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tens
     [N, Hq, D] are the newest tokens of request r."""
     c = _Caches(cache)
     _heads(q, c)
-    _window_prefill(c, _lib.load().qsa_window_prefill, cu_q, ctx_lens, int(max_q_per_req), q, int(window), int(sinks),
-                    float(sm_scale), o, lse, _bytes(workspace, c.index), stream)
+    _window_prefill(c, _lib.load().qsa_window_prefill, cu_q, ctx_lens, _int32(max_q_per_req, "max_q_per_req"), q,
+                    _int32(window, "window"), _int32(sinks, "sinks"), float(sm_scale), o, lse,
+                    _bytes(workspace, c.index), stream)
 
 
 class QSAWindowPrefill:
@@ -239,8 +247,8 @@ class QSAWindowPrefill:
 
     def __init__(self, cache: QSACache, B: int, n_tokens: int, max_q_per_req: int, Hq: int, window: int,
                  sinks: int = 0, sm_scale: float | None = None):
-        self.cache, self.window, self.sinks = cache, int(window), int(sinks)
-        self.B, self.max_q = B, int(max_q_per_req)
+        self.cache, self.window, self.sinks = cache, _int32(window, "window"), _int32(sinks, "sinks")
+        self.B, self.max_q = B, _int32(max_q_per_req, "max_q_per_req")
         c = self._c = _Caches(cache)
         self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
         self.o = torch.zeros((n_tokens, Hq, c.D), dtype=c.dtype, device=c.device)
@@ -281,7 +289,7 @@ def qsa_prefix_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
     c = _Caches(cache)
     _heads(q, c)
     _prefix_decode(c, _lib.load().qsa_prefix_decode, q, ctx_lens, cu_group, prefix_lens,
-                   (int(max_group), int(max_prefix), int(max_tail)), float(sm_scale), o, lse,
+                   tuple(_int32(v, "a bound") for v in (max_group, max_prefix, max_tail)), float(sm_scale), o, lse,
                    _bytes(workspace, c.index), stream)
 
 
@@ -291,7 +299,7 @@ class QSAPrefixDecode:
     def __init__(self, cache: QSACache, B: int, T: int, Hq: int, n_groups: int, max_group: int, max_prefix: int,
                  max_tail: int, sm_scale: float | None = None):
         self.cache, self.n_groups = cache, n_groups
-        self.bounds = (int(max_group), int(max_prefix), int(max_tail))
+        self.bounds = tuple(_int32(v, "a bound") for v in (max_group, max_prefix, max_tail))
         c = self._c = _Caches(cache)
         self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
         self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)

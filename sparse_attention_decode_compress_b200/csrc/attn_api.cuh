@@ -446,6 +446,7 @@ size_t qsa_window_prefill_workspace_bytes(const qsa_cache *cache, int32_t B, int
   if (check_cache(cache) != QSA_OK || B < 1 || n_tokens < 1 || max_q_per_req < 1 || Hq < 1 ||
       Hq % cache->num_kv_heads != 0 || window < 1 || sinks < 0)
     return 0;
+  max_q_per_req = std::min(max_q_per_req, n_tokens);
   return parts_bytes((long long)n_tokens * Hq, plan_chunk(cache, B, max_q_per_req, Hq, window, sinks).splits,
                      cache->head_dim);
 }
@@ -458,7 +459,9 @@ qsa_status qsa_window_prefill(const qsa_cache *cache, int32_t B, int32_t n_token
   if (st != QSA_OK) return st;
   if (B < 0 || n_tokens < 0 || max_q_per_req < 0 || window < 1 || sinks < 0) return QSA_ERR_INVALID_ARG;
   if (B == 0 || n_tokens == 0 || max_q_per_req == 0) return QSA_OK;
-  if (B > 65535) return QSA_ERR_UNSUPPORTED;
+  max_q_per_req = std::min(max_q_per_req, n_tokens);
+  // rows (tokens x heads of a group) are counted in 31 bits
+  if (B > 65535 || (long long)n_tokens * (Hq / cache->num_kv_heads) > 0x7ffffc00LL) return QSA_ERR_UNSUPPORTED;
   if (!cu_q || !q || !ctx_lens || !o || !lse || !aligned(q, 16) || !aligned(o, 16)) return QSA_ERR_INVALID_ARG;
   const size_t need = qsa_window_prefill_workspace_bytes(cache, B, n_tokens, max_q_per_req, Hq, window, sinks);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return QSA_ERR_INVALID_ARG;

@@ -52,7 +52,7 @@ constexpr int kTileThreads = 16 * 32;
 constexpr int kLoadWarp = 8, kMmaWarp = 12;
 constexpr uint32_t kTmemCols = 512;  // S0, S1 at 0 and 128, O0, O1 at 256 and 384
 constexpr float kLazy = 8.f;    // growth of a row's maximum (log2) that is left in the weights
-constexpr unsigned kTileTries = 1u << 25;
+constexpr unsigned long long kTileWaitNs = 2000000000ull;
 
 template <int D>
 struct TileSmem {
@@ -97,13 +97,17 @@ __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase for at most kTileTries tries (a second and more); false
-// when they ran out here or in another role.  (A clock read in the loop, the
-// global timer above all, put 500 cycles into every hand-over between roles.)
+// Waits for the phase, for about kTileWaitNs at most; false when that ran out
+// here or in another role.  (The clock is looked at every 256 tries only: a read
+// of the global timer behind the first try put 500 cycles into every hand-over.)
 __device__ __forceinline__ bool mbar_wait_or(uint64_t *b, uint32_t parity, int *dead) {
-  for (unsigned n = 0; !mbar_try(b, parity); ++n) {
-    if ((n & 1023u) == 1023u && *reinterpret_cast<volatile int *>(dead)) return false;
-    if (n >= kTileTries) {
+  unsigned long long t0 = 0;
+  for (unsigned n = 1; !mbar_try(b, parity); ++n) {
+    if (n & 255u) continue;
+    if (*reinterpret_cast<volatile int *>(dead)) return false;
+    const unsigned long long t = pre::globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kTileWaitNs) {
       *reinterpret_cast<volatile int *>(dead) = 1;
       record_error(kErrTimeout);
       return false;

@@ -192,3 +192,15 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         QSAWindowDecode(c, 2, 1, 4, 16)
     with pytest.raises(ValueError):
         QSARopeAppend(c, 4, rotary_dim=66)
+
+
+@pytest.mark.parametrize("v", [1 << 31, (1 << 32) + 5, -(1 << 31) - 1])
+def test_binding_refuses_what_does_not_fit_32_bits(v):
+    """(ctypes would keep the low 32 bits without a word)"""
+    from sparse_attention_decode_compress_b200 import QSACache, QSAPrefixDecode, QSAWindowDecode, QSAWindowPrefill
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    c = QSACache.allocate(k, k.clone(), torch.zeros((2, 2), dtype=torch.int32), 32, 2)
+    for make in (lambda: QSAWindowDecode(c, 2, 1, 4, v), lambda: QSAWindowDecode(c, 2, 1, 4, 16, v),
+                 lambda: QSAWindowPrefill(c, 2, 8, v, 4, 16), lambda: QSAPrefixDecode(c, 2, 1, 4, 1, 1, v, 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            make()
