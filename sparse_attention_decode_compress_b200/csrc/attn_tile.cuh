@@ -459,35 +459,52 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
   if (warp < kLoadWarp) {
     // ------------------------------------------------------------ softmax --
     regs_up<kRegsSoftmax>();
-    // queries: bf16 rows, 2 D bytes
+    // queries: 16 bytes a thread and load, kStep rows a round of the 256 threads
     {
-      constexpr int kQ = D / 8;  // 16-byte chunks
+      constexpr int kQ = D / 8, kStep = kLoadWarp * 32 / kQ, kBatch = 8;
       const __nv_bfloat16 *qg = static_cast<const __nv_bfloat16 *>(a.q);
-      for (int e = tid; e < tiles * kTileRows * kQ; e += kLoadWarp * 32) {
-        const int rr = e / kQ, ch = e % kQ, m = m0 + rr;
-        const bool ok = rr < rows;
-        const __nv_bfloat16 *src =
-            ok ? qg + ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D + ch * 8 : qg;
-        uint8_t *dst = sm.q[rr / kTileRows] + tile_off(rr % kTileRows, ch);
-        if constexpr (!FP8) {
-          cp_async16_zfill(dst, src, ok);
-        } else {
+      const int ch = tid % kQ;
+      int rr = tid / kQ, tok = (m0 + rr) / a.G, head = (m0 + rr) - tok * a.G;
+      const int dtok = kStep / a.G, dhead = kStep - dtok * a.G;
+      for (int done = 0; done < tiles * kTileRows; done += kBatch * kStep) {
+        uint4 x[kBatch];  // (fp8: a batch of loads in flight, then converted)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const bool ok = rr < rows;
+          const __nv_bfloat16 *src = ok ? qg + ((long long)(sq.tok0 + tok) * a.Hq + g * a.G + head) * D + ch * 8 : qg;
+          if constexpr (!FP8)
+            cp_async16_zfill(sm.q[rr / kTileRows] + tile_off(rr % kTileRows, ch), src, ok);
+          else
+            x[i] = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+          rr += kStep;
+          tok += dtok;
+          head += dhead;
+          if (head >= a.G) {
+            head -= a.G;
+            ++tok;
+          }
+        }
+        if constexpr (FP8) {
           // f16, scaled so that 2^14 <= max |q| 2^e < 2^15; kQ lanes hold a row
-          const uint4 x = ok ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t mxq = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mxq = max(mxq, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          for (int i = 0; i < kBatch; ++i) {
+            const int row = done + i * kStep + tid / kQ;
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t mxq = 0;
 #pragma unroll
-          for (int off = kQ / 2; off >= 1; off >>= 1) mxq = max(mxq, __shfl_xor_sync(0xffffffffu, mxq, off));
-          const int ex = mxq == 0u ? 0 : min(141 - (int)(mxq >> 7), 126);
-          const float f = dec::pow2f(ex);
-          uint32_t h[4];
+            for (int k = 0; k < 4; ++k) mxq = max(mxq, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = dec::pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-          *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-          if (ch == 0) sm.qscale[rr] = dec::pow2f(-ex);
+            for (int off = kQ / 2; off >= 1; off >>= 1) mxq = max(mxq, __shfl_xor_sync(0xffffffffu, mxq, off));
+            const int ex = mxq == 0u ? 0 : min(141 - (int)(mxq >> 7), 126);
+            const float f = dec::pow2f(ex);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = dec::pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+            *reinterpret_cast<uint4 *>(sm.q[row / kTileRows] + tile_off(row % kTileRows, ch)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+            if (ch == 0) sm.qscale[row] = dec::pow2f(-ex);
+          }
         }
       }
       if (!FP8) {
@@ -551,33 +568,57 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
       const long long slot = at * a.slots + a.slot0 + split;
       if (ok) {
         if (live) (a.slots > 1 ? a.lse_part[slot] : a.lse[at]) = lse;
+        if (a.slots == 1) {
+          // bf16 rows: every thread writes its own
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          if (nt > 0) {
-            tmem_ld32(o_at + c, v);
-            pre::tmem_ld_wait();
-          }
-          if (!live) continue;
-          if (a.slots > 1) {
-            if (!some) continue;
-            float *dst = a.o_part + slot * D + c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              store4(dst + e, make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
-                                          __uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv));
-          } else {
+          for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            if (nt > 0) {
+              tmem_ld32(o_at + c, v);
+              pre::tmem_ld_wait();
+            }
+            if (!live) continue;
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.o) + at * D + c;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(some ? __uint_as_float(v[e + 2 * k]) * inv : 0.f,
-                                                               some ? __uint_as_float(v[e + 2 * k + 1]) * inv : 0.f);
-                w[k] = *reinterpret_cast<const uint32_t *>(&b);
-              }
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack16<true>(some ? __uint_as_float(v[e + 2 * k]) * inv : 0.f,
+                                    some ? __uint_as_float(v[e + 2 * k + 1]) * inv : 0.f);
               *reinterpret_cast<uint4 *>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+          // float32 parts, rows far apart: by halves of D, a thread puts its half
+          // into the warp's quarter of the tile's queries, which nothing reads any
+          // more (swizzled by 16 bytes), and the warp writes run after run (a
+          // thread writing its own row took 11,000 cycles)
+          const unsigned rows_out = __ballot_sync(0xffffffffu, live && some);
+          constexpr int kHalf = D / 2, kLanes = kHalf / 4;  // floats, and lanes that write them
+          float *stage = reinterpret_cast<float *>(sm.q[t]) + (warp & 3) * 32 * kHalf;
+          const int l4 = lane % kLanes;
+#pragma unroll 1
+          for (int c0 = 0; nt > 0 && c0 < D; c0 += kHalf) {
+            __syncwarp();  // the half before is read
+#pragma unroll 1
+            for (int c = 0; c < kHalf; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(o_at + c0 + c, v);
+              pre::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                store4(stage + lane * kHalf + (((c + e) / 4) ^ (lane & 7)) * 4,
+                       make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv,
+                                   __uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv));
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int i = 0; i < kLanes; ++i) {
+              const int rr = i * (32 / kLanes) + lane / kLanes;
+              const long long dst = __shfl_sync(0xffffffffu, slot, rr) * D + c0 + 4 * l4;
+              const float4 v = *reinterpret_cast<const float4 *>(stage + rr * kHalf + ((l4 ^ (rr & 7)) * 4));
+              if ((rows_out >> rr) & 1u) store4(a.o_part + dst, v);
             }
           }
         }
