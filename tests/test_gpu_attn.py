@@ -466,3 +466,121 @@ def test_bad_pages_lengths_and_offsets_are_recorded():
     assert torch.equal(before, cache.k_cache)
     y, mag = A.rope_row(q[0, 0], 10 ** 5, rope.inv_freq, 1.0, D, False)
     assert ((out[0].double().cpu() - y).abs() <= 2.0 ** -8 * y.abs() + 2.0 ** -19 * mag).all()
+
+
+# ----------------------------------------------- maxima that move, and NaN --
+def ramped(kv, Hkv, D, page, lens, jumps, seed):
+    """Keys whose first dim jumps at the given positions, so that a row's logits
+    leave the weights' range inside a step, between steps and at its quarters."""
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=seed)
+    for r, L in enumerate(lens):
+        for t in range(L):
+            level = sum(h for at, h in jumps if t >= at)
+            pg, off = int(c.table_host[r, t // page]), t % page
+            if kv == "e4m3":  # by the page's scale: the first code is 448 or 0
+                c.k[pg, off] = c.k[pg, off].float().clamp(-2, 2).to(torch.float8_e4m3fn)
+                c.k_scale[pg] = max(level, 2.0 ** -6) / 448
+                c.k[pg, off, :, 0] = torch.tensor(448.0 if level > 0 else 0.0).to(torch.float8_e4m3fn)
+            else:
+                c.k[pg, off, :, 0] = level
+    return c
+
+
+JUMPS = [[(0, 0.0), (40, 30.0), (70, 25.0), (100, 40.0), (130, 6.0), (250, 90.0)],
+         [(0, 1.0), (16, 20.0), (33, 300.0), (64, 12.0), (128, 500.0), (384, 3.0)],
+         [(0, 400.0), (1, -400.0), (96, 200.0), (97, -100.0)]]
+
+
+@pytest.mark.parametrize("kv,page", [("bf16", 64), ("bf16", 20), ("e4m3", 16), ("f32", 16)])
+@pytest.mark.parametrize("jumps", JUMPS)
+def test_logits_that_jump_along_the_keys(kv, page, jumps):
+    Hq, Hkv, D, dense = 8, 2, 128, 2 ** 31 - 1
+    lens = [450, 300]
+    c = ramped(kv, Hkv, D, page, lens, jumps, seed=81)
+    new = [70, 33]
+    q = queries((sum(new), Hq, D), kv, 82)
+    q[..., 0] = 8.0
+    cache = c.cache()
+    want, _ = chunk_want(c, q, new, lens, dense, 0)
+    o, lse = QSAWindowPrefill(cache, 2, sum(new), max(new), Hq, dense)(q.cuda(), ints([0, 70, 103]), ints(lens))
+    A.check(o, lse, want, kv, D, "chunk")
+    qd = torch.stack([q[66:70], q[99:103]])
+    want, _ = window_want(c, qd, lens, 4, dense, 0)
+    o, lse = QSAWindowDecode(cache, 2, 4, Hq, dense)(qd.cuda(), ints(lens))
+    A.check(o, lse, want, kv, D, "decode")
+    # the prefix of a group of its own, for each
+    o, lse = QSAPrefixDecode(cache, 2, 4, Hq, 2, 1, 256, 250)(qd.cuda(), ints(lens), ints([0, 1, 2]), ints([256, 200]))
+    A.check(o, lse, want, kv, D, "prefix")
+
+
+@pytest.mark.parametrize("kv,page", [("bf16", 64), ("e4m3", 16), ("f32", 16)])
+def test_a_nan_that_a_query_sees_is_in_its_result_and_nowhere_else(kv, page):
+    Hq, Hkv, D = 8, 2, 128
+    lens = [200, 200]
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=91)
+    pg, off = int(c.table_host[1, 150 // page]), 150 % page
+    if kv == "e4m3":
+        c.k.view(torch.uint8)[pg, off, 1, 5] = 0x7F
+    else:
+        c.k[pg, off, 1, 5] = float("nan")
+    cache = c.cache()
+    q = queries((2, 1, Hq, D), kv, 92).cuda()
+    clean = [1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 0, 0, 0, 0]  # request 1's heads of kv head 1 see it
+    clean = torch.tensor(clean, dtype=torch.bool, device="cuda").view(2, 1, Hq)
+    ch = torch.cat([q[:1, 0], q[1:, 0]])
+    for o, lse in (QSAWindowDecode(cache, 2, 1, Hq, 100)(q, ints(lens)),
+                   QSAPrefixDecode(cache, 2, 1, Hq, 2, 1, 160, 40)(q, ints(lens), ints([0, 1, 2]), ints([160, 128])),
+                   QSAWindowPrefill(cache, 2, 2, 1, Hq, 64)(ch, ints([0, 1, 2]), ints(lens))):
+        o, lse = o.view(2, 1, Hq, D), lse.view(2, 1, Hq)
+        assert torch.equal(torch.isfinite(lse), clean)
+        assert torch.equal(torch.isfinite(o).all(-1), clean) and o[~clean].isnan().all() and lse[~clean].isnan().all()
+    # out of the window: nothing of it
+    o, lse = QSAWindowDecode(cache, 2, 1, Hq, 49)(q, ints(lens))
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_prefix_of_many_rows_per_kv_head_and_ragged_groups(kv):
+    """Groups of 1, 70 and 33 requests with two query tokens: partial row tiles
+    of 256, and a group without any."""
+    page, T, Hq, Hkv, D = 32, 2, 8, 2, 64
+    sizes, pages = [1, 70, 0, 33], [3, 11, 2, 7]
+    lens, share, cu, pre = [], {}, [0], []
+    for n, p in zip(sizes, pages):
+        first = len(lens)
+        for i in range(n):
+            if i:
+                share[len(lens)] = (first, p)
+            lens.append(p * page + T + (i * 7) % 45)
+        cu.append(len(lens))
+        pre.append(p * page)
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=95, share=share)
+    q = queries((len(lens), T, Hq, D), kv, 96)
+    op = QSAPrefixDecode(c.cache(), len(lens), T, Hq, 4, 70, max(pre), 47)
+    o, lse = op(q.cuda(), ints(lens), ints(cu), ints(pre))
+    A.check(o, lse, prefix_want(c, q, lens, T), kv, D, "prefix")
+
+
+def test_two_streams_with_handles_of_their_own():
+    """Calls in flight on two streams at once, each with its own handle."""
+    Hq, Hkv, D = 16, 2, 128
+    lens = [3000, 2000]
+    c = A.PagedKV(lens, Hkv, D, "bf16", 64, "cuda", seed=97)
+    cache = c.cache()
+    qs = [queries((2, 1, Hq, D), "bf16", 98 + i).cuda() for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ops = [(QSAWindowDecode(cache, 2, 1, Hq, 2 ** 31 - 1), QSAPrefixDecode(cache, 2, 1, Hq, 1, 1, 1500, 1500))
+           for _ in range(2)]
+    L, cu, pl = ints(lens), ints([0, 1]), ints([1500])
+    alone = []
+    for q, (w, p) in zip(qs, ops):
+        alone.append([t.clone() for t in (*w(q, L), *p(q, L, cu, pl))])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, s, (w, p) in zip(qs, streams, ops):
+            w(q, L, stream=s)
+            p(q, L, cu, pl, stream=s)
+    torch.cuda.synchronize()
+    for want, (w, p) in zip(alone, ops):
+        for a, b in zip(want, (w.o, w.lse, p.o, p.lse)):
+            assert torch.equal(a, b)
