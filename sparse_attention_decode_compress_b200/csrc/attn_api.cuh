@@ -49,13 +49,17 @@ AttnPlan plan_stream(long long seqs, int Hkv, long long span, bool merge) {
   p.tiles = 1;
   const long long pairs = std::max(1LL, seqs * Hkv);
   if (merge) {
-    // two CTAs an SM; up to 8 of a row form a cluster, also where there is
-    // room for more, up to 1,024 keys each
+    // two CTAs an SM (batch 32 x 32k, window 4,096: 39.6 us a single pass against
+    // 43.1 with four and 47.5 with eight), none with more than 16,384 keys; up to 8
+    // of a row form a cluster, also where there is room for more, up to 1,024 keys
+    // each
     p.splits = (int)std::max(1LL, std::min({2LL * kPlanSMs / pairs, ceil_ll(span, 128), 64LL}));
+    p.splits = (int)std::max<long long>(p.splits, std::min(ceil_ll(span, 16384), 64LL));
     if (p.splits > kMaxCluster && span <= 1024LL * kMaxCluster) p.splits = kMaxCluster;
     p.cluster = p.splits > 1 && p.splits <= kMaxCluster;
   } else {
-    // tails of very different lengths: more and smaller pieces
+    // tails of very different lengths: more and smaller pieces (128 tails of 1
+    // to 8,192 keys behind one prefix: 292 us in all against 308 with half as many)
     p.splits = (int)std::max(1LL, std::min({8LL * kPlanSMs / pairs, ceil_ll(span, 256), 64LL}));
   }
   return p;
@@ -67,8 +71,10 @@ AttnPlan plan_tiles(long long seqs, int Hkv, long long rows, long long span) {
   AttnPlan p = {};
   p.tiles = ceil_ll(std::max(rows, 1LL), 2 * qsa::attn::kTileRows);
   const long long ctas = std::max(1LL, seqs * Hkv * p.tiles);
-  // one wave while that leaves a split 16 tiles of keys; otherwise about two,
-  // so that sequences of different lengths even out
+  // one wave of CTAs for one sequence; about two for several, whose lengths may
+  // differ (eight fp8 prefixes of 3,001 to 16,384 keys: 174 us against 179 with one
+  // wave and 196 with three); a split takes four tiles of keys at least (eight:
+  // 60 against 54 us for one prefix of 28,672)
   const long long waves = seqs > 1 && ctas < kPlanSMs ? 2 : 1;
   p.splits = (int)std::max(1LL, std::min({waves * kPlanSMs / ctas, ceil_ll(span, 4 * qsa::attn::kTileKeys), 64LL}));
   return p;
@@ -294,8 +300,9 @@ qsa_status launch_rope(const qsa::rope::Params &p, bool vec, int layout, cudaStr
   constexpr int kStep = 32 / (D / 16);
   constexpr int NB = sizeof(T) == 4 ? 2 : 5;
   const long long few = (long long)p.n_tok * ceil_ll(heads, kStep);
-  // one step a warp while that leaves the GPU room (few tokens: latency), NB
-  // steps, all loaded at once, for more
+  // one step a warp while that leaves the GPU room (128 tokens: latency), NB steps,
+  // all loaded at once, for more: 22,000 tokens of 40 heads take 99 us with one,
+  // 76, 74, 73 and 72 with two to five (four times the registers from there on)
   const bool one = few <= 16LL * kPlanSMs;
   const long long warps = (long long)p.n_tok * ceil_ll(heads, kStep * (one ? 1 : NB));
   const long long grid = ceil_ll(warps * 32, kThreads);

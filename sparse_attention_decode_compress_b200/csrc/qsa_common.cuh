@@ -14,7 +14,7 @@ namespace qsa {
 // Error bits of the per-device error word (read by qsa_get_device_error).
 enum : uint32_t {
   kErrBounds = 1u,    // block-table entry / logical page / position out of range
-  kErrTimeout = 2u,   // a bounded wait ran out (kept for the ABI; no kernel of this version waits)
+  kErrTimeout = 2u,   // a bounded wait ran out
   kErrBadInput = 4u,  // malformed lengths, counts or selection rows
 };
 
