@@ -82,6 +82,11 @@ def _workspace(nbytes: int, device) -> torch.Tensor | None:
     return new_workspace(nbytes, device) if nbytes else None
 
 
+def _outputs(c: _Caches, shape, o: torch.Tensor, lse: torch.Tensor) -> tuple[int, int]:
+    return (_dense(o, c.dtype, shape, "o", c.index),
+            _dense(lse, torch.float32, shape[:-1], "lse", c.index))
+
+
 def _heads(q: torch.Tensor, c: _Caches) -> None:
     if q.shape[-1] != c.D:
         raise ValueError("q and the cache have different head dims")
@@ -175,14 +180,6 @@ def qsa_window_decode_workspace_bytes(cache: QSACache, B: int, T: int, Hq: int, 
     return int(_lib.load().qsa_window_decode_workspace_bytes(ctypes.byref(cache.struct()), B, T, Hq, window, sinks))
 
 
-def _window_decode(c: _Caches, fn, q, ctx_lens, window, sinks, sm_scale, o, lse, ws, stream):
-    B, T, Hq, D = shape = q.shape
-    dt, ix = c.dtype, c.index
-    _call(fn, "qsa_window_decode", ix,
-          (c.ref, B, T, Hq, _dense(q, dt, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix), window, sinks,
-           sm_scale, _dense(o, dt, shape, "o", ix), _dense(lse, torch.float32, shape[:3], "lse", ix), *ws), stream)
-
-
 def qsa_window_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, window: int, sinks: int,
                       sm_scale: float, o: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor | None,
                       stream=None) -> None:
@@ -190,8 +187,12 @@ def qsa_window_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
     keys and first `sinks` keys.  o: q's type and shape, lse float32."""
     c = _Caches(cache)
     _heads(q, c)
-    _window_decode(c, _lib.load().qsa_window_decode, q, ctx_lens, _int32(window, "window"), _int32(sinks, "sinks"),
-                   float(sm_scale), o, lse, _bytes(workspace, c.index), stream)
+    B, T, Hq, _ = shape = q.shape
+    ix = c.index
+    _call(_lib.load().qsa_window_decode, "qsa_window_decode", ix,
+          (c.ref, B, T, Hq, _dense(q, c.dtype, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix),
+           _int32(window, "window"), _int32(sinks, "sinks"), float(sm_scale), *_outputs(c, shape, o, lse),
+           *_bytes(workspace, ix)), stream)
 
 
 class QSAWindowDecode:
@@ -205,13 +206,16 @@ class QSAWindowDecode:
         self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)
         self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=c.device)
         self.ws = _workspace(qsa_window_decode_workspace_bytes(cache, B, T, Hq, self.window, self.sinks), c.device)
-        self._ws, self._fn = _bytes(self.ws, c.index), _lib.load().qsa_window_decode
+        self._shape, self._fn = self.o.shape, _lib.load().qsa_window_decode
+        self._head = (c.ref, B, T, Hq)
+        self._tail = (self.window, self.sinks, self.sm_scale, *_outputs(c, self._shape, self.o, self.lse),
+                      *_bytes(self.ws, c.index))
 
     def __call__(self, q, ctx_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-        if q.shape != self.o.shape:
-            raise ValueError(f"q must be {list(self.o.shape)}")
-        _window_decode(self._c, self._fn, q, ctx_lens, self.window, self.sinks, self.sm_scale, self.o, self.lse,
-                       self._ws, stream)
+        c = self._c
+        _call(self._fn, "qsa_window_decode", c.index,
+              (*self._head, _dense(q, c.dtype, self._shape, "q", c.index), c.qd,
+               _ints(ctx_lens, self._shape[0], "ctx_lens", c.index), *self._tail), stream)
         return self.o, self.lse
 
 
@@ -221,15 +225,6 @@ def qsa_window_prefill_workspace_bytes(cache: QSACache, B: int, n_tokens: int, m
                                                               max_q_per_req, Hq, window, sinks))
 
 
-def _window_prefill(c: _Caches, fn, cu_q, ctx_lens, max_q, q, window, sinks, sm_scale, o, lse, ws, stream):
-    n, Hq, D = shape = q.shape
-    B, dt, ix = ctx_lens.shape[0], c.dtype, c.index
-    _call(fn, "qsa_window_prefill", ix,
-          (c.ref, B, n, max_q, _ints(cu_q, B + 1, "cu_q", ix), _ints(ctx_lens, B, "ctx_lens", ix),
-           _dense(q, dt, shape, "q", ix), c.qd, Hq, window, sinks, sm_scale, _dense(o, dt, shape, "o", ix),
-           _dense(lse, torch.float32, shape[:2], "lse", ix), *ws), stream)
-
-
 def qsa_window_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tensor, max_q_per_req: int,
                        q: torch.Tensor, window: int, sinks: int, sm_scale: float, o: torch.Tensor,
                        lse: torch.Tensor, workspace: torch.Tensor | None, stream=None) -> None:
@@ -237,9 +232,12 @@ def qsa_window_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tens
     [N, Hq, D] are the newest tokens of request r."""
     c = _Caches(cache)
     _heads(q, c)
-    _window_prefill(c, _lib.load().qsa_window_prefill, cu_q, ctx_lens, _int32(max_q_per_req, "max_q_per_req"), q,
-                    _int32(window, "window"), _int32(sinks, "sinks"), float(sm_scale), o, lse,
-                    _bytes(workspace, c.index), stream)
+    n, Hq, _ = shape = q.shape
+    B, ix = ctx_lens.shape[0], c.index
+    _call(_lib.load().qsa_window_prefill, "qsa_window_prefill", ix,
+          (c.ref, B, n, _int32(max_q_per_req, "max_q_per_req"), _ints(cu_q, B + 1, "cu_q", ix),
+           _ints(ctx_lens, B, "ctx_lens", ix), _dense(q, c.dtype, shape, "q", ix), c.qd, Hq, _int32(window, "window"),
+           _int32(sinks, "sinks"), float(sm_scale), *_outputs(c, shape, o, lse), *_bytes(workspace, ix)), stream)
 
 
 class QSAWindowPrefill:
@@ -255,13 +253,16 @@ class QSAWindowPrefill:
         self.lse = torch.full((n_tokens, Hq), -math.inf, dtype=torch.float32, device=c.device)
         self.ws = _workspace(qsa_window_prefill_workspace_bytes(cache, B, n_tokens, self.max_q, Hq, self.window,
                                                                 self.sinks), c.device)
-        self._ws, self._fn = _bytes(self.ws, c.index), _lib.load().qsa_window_prefill
+        self._shape, self._fn = self.o.shape, _lib.load().qsa_window_prefill
+        self._head = (c.ref, B, n_tokens, self.max_q)
+        self._tail = (c.qd, Hq, self.window, self.sinks, self.sm_scale,
+                      *_outputs(c, self._shape, self.o, self.lse), *_bytes(self.ws, c.index))
 
     def __call__(self, q, cu_q, ctx_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-        if q.shape != self.o.shape or ctx_lens.shape != (self.B,):
-            raise ValueError(f"q must be {list(self.o.shape)} and ctx_lens [{self.B}]")
-        _window_prefill(self._c, self._fn, cu_q, ctx_lens, self.max_q, q, self.window, self.sinks, self.sm_scale,
-                        self.o, self.lse, self._ws, stream)
+        c = self._c
+        _call(self._fn, "qsa_window_prefill", c.index,
+              (*self._head, _ints(cu_q, self.B + 1, "cu_q", c.index), _ints(ctx_lens, self.B, "ctx_lens", c.index),
+               _dense(q, c.dtype, self._shape, "q", c.index), *self._tail), stream)
         return self.o, self.lse
 
 
@@ -272,15 +273,6 @@ def qsa_prefix_decode_workspace_bytes(cache: QSACache, B: int, T: int, Hq: int, 
                                                              max_group, max_prefix, max_tail))
 
 
-def _prefix_decode(c: _Caches, fn, q, ctx_lens, cu_group, prefix_lens, bounds, sm_scale, o, lse, ws, stream):
-    B, T, Hq, D = shape = q.shape
-    n, dt, ix = prefix_lens.shape[0], c.dtype, c.index
-    _call(fn, "qsa_prefix_decode", ix,
-          (c.ref, B, T, Hq, _dense(q, dt, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix), n,
-           _ints(cu_group, n + 1, "cu_group", ix), _ints(prefix_lens, n, "prefix_lens", ix), *bounds, sm_scale,
-           _dense(o, dt, shape, "o", ix), _dense(lse, torch.float32, shape[:3], "lse", ix), *ws), stream)
-
-
 def qsa_prefix_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, cu_group: torch.Tensor,
                       prefix_lens: torch.Tensor, max_group: int, max_prefix: int, max_tail: int, sm_scale: float,
                       o: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
@@ -288,9 +280,13 @@ def qsa_prefix_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
     their first prefix_lens[g] keys."""
     c = _Caches(cache)
     _heads(q, c)
-    _prefix_decode(c, _lib.load().qsa_prefix_decode, q, ctx_lens, cu_group, prefix_lens,
-                   tuple(_int32(v, "a bound") for v in (max_group, max_prefix, max_tail)), float(sm_scale), o, lse,
-                   _bytes(workspace, c.index), stream)
+    B, T, Hq, _ = shape = q.shape
+    n, ix = prefix_lens.shape[0], c.index
+    _call(_lib.load().qsa_prefix_decode, "qsa_prefix_decode", ix,
+          (c.ref, B, T, Hq, _dense(q, c.dtype, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix), n,
+           _ints(cu_group, n + 1, "cu_group", ix), _ints(prefix_lens, n, "prefix_lens", ix),
+           *(_int32(v, "a bound") for v in (max_group, max_prefix, max_tail)), float(sm_scale),
+           *_outputs(c, shape, o, lse), *_bytes(workspace, ix)), stream)
 
 
 class QSAPrefixDecode:
@@ -305,11 +301,16 @@ class QSAPrefixDecode:
         self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)
         self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=c.device)
         self.ws = _workspace(qsa_prefix_decode_workspace_bytes(cache, B, T, Hq, n_groups, *self.bounds), c.device)
-        self._ws, self._fn = _bytes(self.ws, c.index), _lib.load().qsa_prefix_decode
+        self._shape, self._fn = self.o.shape, _lib.load().qsa_prefix_decode
+        self._head = (c.ref, B, T, Hq)
+        self._tail = (*self.bounds, self.sm_scale, *_outputs(c, self._shape, self.o, self.lse),
+                      *_bytes(self.ws, c.index))
 
     def __call__(self, q, ctx_lens, cu_group, prefix_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-        if q.shape != self.o.shape or prefix_lens.shape != (self.n_groups,):
-            raise ValueError(f"q must be {list(self.o.shape)} and prefix_lens [{self.n_groups}]")
-        _prefix_decode(self._c, self._fn, q, ctx_lens, cu_group, prefix_lens, self.bounds, self.sm_scale, self.o,
-                       self.lse, self._ws, stream)
+        c, n = self._c, self.n_groups
+        _call(self._fn, "qsa_prefix_decode", c.index,
+              (*self._head, _dense(q, c.dtype, self._shape, "q", c.index), c.qd,
+               _ints(ctx_lens, self._shape[0], "ctx_lens", c.index), n,
+               _ints(cu_group, n + 1, "cu_group", c.index), _ints(prefix_lens, n, "prefix_lens", c.index),
+               *self._tail), stream)
         return self.o, self.lse

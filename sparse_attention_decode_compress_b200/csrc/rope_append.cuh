@@ -18,6 +18,10 @@
 // token (or a share of its heads): the two angles a lane computes are passed
 // around by shuffles, every lane keeps the 8 (cos, sin) pairs of its place in
 // the head and applies them to one head after another, 16 bytes at a time.
+// Measured (B200): 22,152 tokens of 32 / 4 heads, D 128, bf16: 72.8 us, 6.2 TB/s
+// (97 % of the measured copy rate); 4,096 tokens of 16 / 2 heads: 11.3 us (one
+// wave of warps, whose chain request -> position -> page -> store is exposed);
+// 128 tokens: 2.8 us in a graph.
 #pragma once
 #include "qsa_common.cuh"
 
@@ -60,6 +64,14 @@ __device__ __forceinline__ void sincos_turns(uint64_t phase, float m, float &s, 
   sincospif(x, &s, &c);
   s *= m;
   c *= m;
+}
+
+// A pair turned by (c, s) = m (cos, sin); the same roundings in every form of
+// the kernel.
+__device__ __forceinline__ void turn_pair(float &a, float &b, float c, float s) {
+  const float x = a;
+  a = __fmaf_rn(x, c, -__fmul_rn(b, s));
+  b = __fmaf_rn(x, s, __fmul_rn(b, c));
 }
 
 // 8 consecutive elements as float32 and back.
@@ -190,19 +202,12 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(Params p) {
       if (INTERLEAVED) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float a0 = a[2 * i], b0 = b[2 * i];
-          a[2 * i] = a0 * c8[i] - a[2 * i + 1] * s8[i];
-          a[2 * i + 1] = a0 * s8[i] + a[2 * i + 1] * c8[i];
-          b[2 * i] = b0 * c8[4 + i] - b[2 * i + 1] * s8[4 + i];
-          b[2 * i + 1] = b0 * s8[4 + i] + b[2 * i + 1] * c8[4 + i];
+          turn_pair(a[2 * i], a[2 * i + 1], c8[i], s8[i]);
+          turn_pair(b[2 * i], b[2 * i + 1], c8[4 + i], s8[4 + i]);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a0 = a[i];
-          a[i] = a0 * c8[i] - b[i] * s8[i];
-          b[i] = a0 * s8[i] + b[i] * c8[i];
-        }
+        for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], c8[i], s8[i]);
       }
     }
     if (h < p.Hq) {
@@ -246,11 +251,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_any_kernel(Params p, int
                      : h < p.Hq + Hk ? static_cast<const T *>(p.k) + tok * p.k_stride + (h - p.Hq) * D
                                      : static_cast<const T *>(p.v) + tok * p.v_stride + (h - p.Hq - Hk) * D;
       float a = to_f(src[i0]), b = to_f(src[i1]);
-      if (pair && h < p.Hq + Hk) {
-        const float a0 = a;
-        a = a0 * cs - b * sn;
-        b = a0 * sn + b * cs;
-      }
+      if (pair && h < p.Hq + Hk) turn_pair(a, b, cs, sn);
       if (h < p.Hq) {
         T *dst = static_cast<T *>(p.q_out) + ((long long)tok * p.Hq + h) * D;
         st1(dst + i0, a, 1.f);

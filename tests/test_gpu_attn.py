@@ -323,6 +323,29 @@ def test_rope_append(kv, Hq, Hkv, D, page, R, interleaved, scaling, factor, fuse
     assert torch.equal(got_k[~touched], want_k[~touched]) and torch.equal(got_v[~touched], want_v[~touched])
 
 
+@pytest.mark.parametrize("offset,pad", [(0, 1), (1, 0), (3, 8)])
+def test_rope_rows_of_any_alignment(offset, pad):
+    """Rows that are not 16 bytes aligned, by their start or their stride, give
+    the bits of aligned ones; 1,500 requests, some without a token."""
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    new = [i % 3 for i in range(1500)]
+    pos0 = [(i * 37) % 300 for i in range(1500)]
+    n = sum(new)
+    c = A.PagedKV([p + 3 for p in pos0], Hkv, D, "bf16", page, "cuda", seed=25)
+    width = (Hq + 2 * Hkv) * D
+    buf = queries((n * (width + pad) + offset,), "bf16", 26).cuda()
+    rows = buf[offset:].view(n, width + pad)[:, :width].unflatten(1, (Hq + 2 * Hkv, D))
+    cu = ints(np.concatenate([[0], np.cumsum(new)]).tolist())
+    outs = []
+    for x in (rows, rows.contiguous()):
+        cache = c.cache()
+        op = QSARopeAppend(cache, Hq, 32, interleaved=True)
+        q = op(ints(pos0), cu, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:])
+        outs.append((q, cache.k_cache, cache.v_cache))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
 def test_rope_far_positions_and_in_place():
     """Angles at positions around two billion, and q rotated in place."""
     page, D = 64, 128
