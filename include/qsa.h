@@ -557,7 +557,7 @@ qsa_status qsa_rope_append(const qsa_cache *cache, int32_t B, int32_t n_tokens, 
  *
  *   q    [B, T, Hq, D], T 1 .. 4, (Hq / Hkv) * T <= 32, 16-byte aligned
  *   ctx_lens [B] int32 cached tokens (>= T; shorter: the query tokens before
- *            position 0 see nothing)
+ *            position 0 see nothing; a negative length counts as 0)
  *   window >= 1, sinks >= 0
  *   o    [B, T, Hq, D] of q_dtype, 16-byte aligned;  lse [B, T, Hq] float32
  *   workspace >= qsa_window_decode_workspace_bytes(...) (the cache's geometry

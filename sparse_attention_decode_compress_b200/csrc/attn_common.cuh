@@ -67,6 +67,15 @@ struct Seq {
   bool grouped;    // kTail: the request belongs to a group
 };
 
+// Cached tokens of request r; a negative length counts as none.
+__device__ __forceinline__ int ctx_len(const Args &a, int r) { return max(a.ctx_lens[r], 0); }
+
+// First key in the window of the query at position p.  Positions before 0 (a
+// request with fewer cached tokens than query tokens) count as -1, whose window
+// ends before key 0: nothing is subtracted from them, so window = INT32_MAX stays
+// within 32 bits.
+__device__ __forceinline__ int window_lo(int p, int window) { return max(0, max(p + 1, 0) - window); }
+
 // Sequence s; a malformed description (offsets that fall or leave the query
 // rows) is recorded and gives an empty sequence.
 template <int MODE>
@@ -98,12 +107,12 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     }
     q.tok0 = t0;
     q.ntok = t1 - t0;
-    q.first = a.ctx_lens[s] - q.ntok;
+    q.first = ctx_len(a, s) - q.ntok;
     return q;
   }
   q.tok0 = s * a.T;
   q.ntok = a.T;
-  q.first = a.ctx_lens[s] - a.T;
+  q.first = ctx_len(a, s) - a.T;
   if (MODE == kTail) {
     // the group that holds request s: the last one that starts at or before it
     int lo = 0, hi = a.n_cu;
@@ -131,14 +140,14 @@ __device__ __forceinline__ Seen seen_by(const Args &a, const Seq &q, int i) {
   v.lo = 0;
   if (MODE == kShared) {
     const int tok = q.tok0 + i, r = tok / a.T;
-    v.hi = min(q.prefix, a.ctx_lens[r] - a.T + (tok - r * a.T) + 1);
+    v.hi = min(q.prefix, ctx_len(a, r) - a.T + (tok - r * a.T) + 1);
     return v;
   }
   v.hi = q.first + i + 1;
   if (MODE == kTail) {
     v.lo = q.prefix;
   } else {
-    v.lo = max(0, v.hi - a.window);
+    v.lo = window_lo(q.first + i, a.window);
     v.sink = a.sinks;
   }
   return v;
@@ -187,7 +196,7 @@ __device__ __forceinline__ Range range_of(const Args &a, const Seq &q, int i0, i
     hi = q.prefix;  // a query before the prefix's end masks what it does not see
   } else {
     hi = q.first + i1;
-    lo = MODE == kTail ? q.prefix : max(0, q.first + i0 + 1 - a.window);
+    lo = MODE == kTail ? q.prefix : window_lo(q.first + i0, a.window);
     sink = MODE == kTail ? 0 : a.sinks;
   }
   if (hi <= 0) return r;

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
     // the keys that some query of the request sees are loaded, the others of
     // a group of four (and past the end) are zero
     Seen any = seen_by<MODE>(a, sq, a.T - 1);
-    if (MODE == kWindow) any.lo = max(0, sq.first + 1 - a.window);
+    if (MODE == kWindow) any.lo = window_lo(sq.first, a.window);
     // ---- issue of stage s (keys w0 + 16 s ..) into its slot
     auto issue = [&](int s) {
       const int xs = w0 + s * kStageKeys;

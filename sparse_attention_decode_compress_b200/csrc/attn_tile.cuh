@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
                               static_cast<const uint8_t *>(a.c.v_cache) + (long long)g * kRowBytes};
     // keys that some row of the CTA sees; the others are zero
     Seen any = seen_by<MODE>(a, sq, i1 - 1);
-    if (MODE == kWindow) any.lo = max(0, sq.first + i0 + 1 - a.window);
+    if (MODE == kWindow) any.lo = window_lo(sq.first + i0, a.window);
     if (MODE == kShared) any.hi = sq.prefix;
     // lane i < 8: the block-table entry of this warp's keys 4 i .. 4 i + 3 of a
     // tile, loaded a step ahead of its use (-1: none is needed)

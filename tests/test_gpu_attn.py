@@ -607,3 +607,46 @@ def test_two_streams_with_handles_of_their_own():
     for want, (w, p) in zip(alone, ops):
         for a, b in zip(want, (w.o, w.lse, p.o, p.lse)):
             assert torch.equal(a, b)
+
+
+# ------------------------------------- contexts shorter than their queries --
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("sinks", [0, 2])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 3])
+def test_contexts_shorter_than_the_query_tokens(kv, sinks, window):
+    """Query tokens before position 0 see nothing and take nothing from the
+    others, at any window: four decode tokens over 0 to 4 cached ones, and
+    chunks longer than their contexts."""
+    Hq, Hkv, D, T = 8, 2, 128, 4
+    lens = [0, 1, 2, 3, 4, 9]
+    c = A.PagedKV(lens, Hkv, D, kv, 16, "cuda", seed=101)
+    q = queries((len(lens), T, Hq, D), kv, 102)
+    want, seen = window_want(c, q, lens, T, window, sinks)
+    c.poison(seen)
+    o, lse = QSAWindowDecode(c.cache(), len(lens), T, Hq, window, sinks)(q.cuda(), ints(lens))
+    A.check(o, lse, want, kv, D, "decode")
+    new, lens = [8, 8, 200, 5], [5, 0, 3, 9]  # 200 tokens: row tiles without a token at position 0 or later
+    c = A.PagedKV(lens, Hkv, D, kv, 16, "cuda", seed=103)
+    q = queries((sum(new), Hq, D), kv, 104)
+    want, seen = chunk_want(c, q, new, lens, window, sinks)
+    c.poison(seen)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    o, lse = QSAWindowPrefill(c.cache(), 4, sum(new), max(new), Hq, window, sinks)(q.cuda(), ints(cu), ints(lens))
+    A.check(o, lse, want, kv, D, "chunk")
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+def test_a_negative_length_is_an_empty_request(kv):
+    Hq, Hkv, D, T = 8, 2, 128, 4
+    c = A.PagedKV([60, 60, 60], Hkv, D, kv, 16, "cuda", seed=105)
+    q = queries((3, T, Hq, D), kv, 106)
+    lens, dense = [-1, 60, -2 ** 31], 2 ** 31 - 1
+    want, _ = window_want(c, q, [0, 60, 0], T, dense, 0)
+    cache = c.cache()
+    o, lse = QSAWindowDecode(cache, 3, T, Hq, dense)(q.cuda(), ints(lens))
+    A.check(o, lse, want, kv, D, "decode")
+    o, lse = QSAPrefixDecode(cache, 3, T, Hq, 3, 1, 32, 32)(q.cuda(), ints(lens), ints([0, 1, 2, 3]), ints([32] * 3))
+    A.check(o, lse, want, kv, D, "prefix")
+    want, _ = chunk_want(c, q.flatten(0, 1), [T] * 3, [0, 60, 0], dense, 0)
+    o, lse = QSAWindowPrefill(cache, 3, 3 * T, T, Hq, dense)(q.flatten(0, 1).cuda(), ints([0, 4, 8, 12]), ints(lens))
+    A.check(o, lse, want, kv, D, "chunk")
