@@ -614,6 +614,9 @@ qsa_status qsa_window_prefill(const qsa_cache *cache, int32_t B, int32_t n_token
  *            nothing; a group may be empty, a prefix 0
  *   max_group   host bound of a group's requests, 1 .. B; a larger group is
  *               recorded as QSA_ERR_BAD_INPUT and its prefix left out
+ *               (its requests get their tails alone), as is a group whose
+ *               offsets fall or leave the batch; a negative prefix is
+ *               recorded and counts as 0
  *   max_prefix, max_tail  expected bounds of prefix_lens and of
  *               ctx_lens - prefix_lens (they only choose how the work is
  *               split: longer ones are right, and slower)

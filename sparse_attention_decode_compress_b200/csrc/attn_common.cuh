@@ -64,7 +64,7 @@ struct Seq {
   int table;       // its block-table row
   int first;       // kWindow / kTail: position of its first query token
   int prefix;      // kShared / kTail: keys of the shared prefix
-  bool grouped;    // kTail: the request belongs to a group
+  bool shared;     // kTail: the prefixes' kernel writes the request's first slots
 };
 
 // Cached tokens of request r; a negative length counts as none.
@@ -76,6 +76,12 @@ __device__ __forceinline__ int ctx_len(const Args &a, int r) { return max(a.ctx_
 // within 32 bits.
 __device__ __forceinline__ int window_lo(int p, int window) { return max(0, max(p + 1, 0) - window); }
 
+// Requests r0 .. r1 - 1 and a prefix as a group that the prefixes' kernel takes.
+// Its tails ask the same, so that a refused group's slots get their empty lse.
+__device__ __forceinline__ bool group_ok(const Args &a, int r0, int r1, int prefix) {
+  return r0 >= 0 && r1 >= r0 && r1 <= a.B && prefix >= 0 && (r1 - r0) * a.T <= a.max_tokens;
+}
+
 // Sequence s; a malformed description (offsets that fall or leave the query
 // rows) is recorded and gives an empty sequence.
 template <int MODE>
@@ -84,11 +90,11 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
   q.table = s;
   q.prefix = 0;
   q.first = 0;
-  q.grouped = false;
+  q.shared = false;
   if (MODE == kShared) {
     const int r0 = a.cu[s], r1 = a.cu[s + 1];
     q.prefix = a.prefix_lens[s];
-    if (r0 < 0 || r1 < r0 || r1 > a.B || q.prefix < 0 || (r1 - r0) * a.T > a.max_tokens) {
+    if (!group_ok(a, r0, r1, q.prefix)) {
       record_error(kErrBadInput);
       q.tok0 = q.ntok = 0;
       return q;
@@ -121,9 +127,14 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
       if (a.cu[mid] <= s) lo = mid;
       else hi = mid;
     }
-    // a request outside every group shares nothing
-    q.grouped = a.cu[lo] <= s && s < a.cu[lo + 1];
-    if (q.grouped) q.prefix = max(a.prefix_lens[lo], 0);
+    // a request outside every group shares nothing, one of a refused group loses
+    // its prefix
+    const int r0 = a.cu[lo], r1 = a.cu[lo + 1];
+    if (r0 <= s && s < r1) {
+      const int prefix = a.prefix_lens[lo];
+      q.prefix = max(prefix, 0);
+      q.shared = group_ok(a, r0, r1, prefix);
+    }
   }
   return q;
 }

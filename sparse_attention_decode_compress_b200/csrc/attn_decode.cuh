@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
       if (l != 0.f) store4(a.o_part + slot * D + d, acc);
       if (d == 0) {
         a.lse_part[slot] = lse;
-        if (MODE == kTail && split == 0 && !sq.grouped)
+        if (MODE == kTail && split == 0 && !sq.shared)
           for (int k = 0; k < a.slot0; ++k) a.lse_part[at * a.slots + k] = -INFINITY;
       }
     } else {

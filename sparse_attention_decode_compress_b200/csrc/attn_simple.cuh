@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
     if (a.slots > 1) {
       const long long slot = at * a.slots + a.slot0 + split;
       if (lane == 0) a.lse_part[slot] = lse;
-      // a request outside every group: nothing else writes its shared slots
-      if (MODE == kTail && split == 0 && !sq.grouped)
+      // outside every group, or in a refused one: nothing else writes the shared slots
+      if (MODE == kTail && split == 0 && !sq.shared)
         for (int k = lane; k < a.slot0; k += 32) a.lse_part[at * a.slots + k] = -INFINITY;
       if (t != 0.f) {
 #pragma unroll

@@ -650,3 +650,34 @@ def test_a_negative_length_is_an_empty_request(kv):
     want, _ = chunk_want(c, q.flatten(0, 1), [T] * 3, [0, 60, 0], dense, 0)
     o, lse = QSAWindowPrefill(cache, 3, 3 * T, T, Hq, dense)(q.flatten(0, 1).cuda(), ints([0, 4, 8, 12]), ints(lens))
     A.check(o, lse, want, kv, D, "chunk")
+
+
+# ------------------------------------------- refused groups and sequences --
+def garbage(op):
+    """Finite values in every partial result that a call could take for its own."""
+    if op.ws is not None:
+        op.ws.view(torch.float32).fill_(7.0)
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("cu,prefix,max_group,bad",
+                         [([0, 2], 64, 1, True),      # larger than max_group
+                          ([0, 3], 64, 2, True),      # leaves the batch
+                          ([-1, 2], 64, 2, True),
+                          ([1, 0], 64, 2, True),      # falls: holds nobody
+                          ([0, 1], -5, 1, True),      # a negative prefix is none
+                          ([0, 2], 64, 2, False)])
+def test_a_refused_group_gives_its_tails(kv, cu, prefix, max_group, bad):
+    Hq, Hkv, D, page, lens = 16, 2, 128, 64, [100, 200]
+    c = A.PagedKV(lens, Hkv, D, kv, page, "cuda", seed=111, share={1: (0, 1)})
+    q = queries((2, 1, Hq, D), kv, 112)
+    op = QSAPrefixDecode(c.cache(), 2, 1, Hq, 1, max_group, 64, 200)
+    rows = []
+    for r, L in enumerate(lens):
+        lo = max(prefix, 0) if bad and cu[0] <= r < cu[1] else 0
+        K, V = (c.values(x, r, range(lo, L)) for x in "kv")
+        rows.append(A.stack([A.attend(q[r, 0], K, V, D ** -0.5)]))
+    garbage(op)
+    o, lse = op(q.cuda(), ints(lens), ints(cu), ints([prefix]))
+    A.check(o, lse, A.stack(rows), kv, D, "tails")
+    assert qsa_get_device_error()[1] == (4 if bad else 0)
