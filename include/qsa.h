@@ -579,7 +579,8 @@ qsa_status qsa_window_decode(const qsa_cache *cache, int32_t B, int32_t T, int32
  * n_r = cu_q[r+1] - cu_q[r] tokens of each request are its query tokens (their
  * K/V rows are in the cache), token j at position ctx_lens[r] - n_r + j.
  *
- *   cu_q [B+1] int32 (cu_q[0] = 0);  rows from cu_q[B] on are left as they were
+ *   cu_q [B+1] int32 (cu_q[0] = 0);  rows from cu_q[B] on are left as they were,
+ *                  and so are the rows of a request whose offsets are refused
  *   n_tokens       rows of q, o and lse
  *   max_q_per_req  host bound of n_r; a longer request is left out
  *                  (QSA_ERR_BAD_INPUT on the device)

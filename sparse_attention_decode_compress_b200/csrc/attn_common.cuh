@@ -76,6 +76,11 @@ __device__ __forceinline__ int ctx_len(const Args &a, int r) { return max(a.ctx_
 // within 32 bits.
 __device__ __forceinline__ int window_lo(int p, int window) { return max(0, max(p + 1, 0) - window); }
 
+// Query tokens t0 .. t1 - 1 as a request of a chunk that the attention kernels take.
+__device__ __forceinline__ bool chunk_ok(const Args &a, int t0, int t1) {
+  return t0 >= 0 && t1 >= t0 && t1 <= a.n_tok && t1 - t0 <= a.max_tokens;
+}
+
 // Requests r0 .. r1 - 1 and a prefix as a group that the prefixes' kernel takes.
 // Its tails ask the same, so that a refused group's slots get their empty lse.
 __device__ __forceinline__ bool group_ok(const Args &a, int r0, int r1, int prefix) {
@@ -106,7 +111,7 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
   }
   if (MODE == kWindow && a.cu) {
     const int t0 = a.cu[s], t1 = a.cu[s + 1];
-    if (t0 < 0 || t1 < t0 || t1 > a.n_tok || t1 - t0 > a.max_tokens) {
+    if (!chunk_ok(a, t0, t1)) {
       record_error(kErrBadInput);
       q.tok0 = q.ntok = 0;
       return q;
@@ -269,13 +274,28 @@ constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeFew = 16;
 constexpr int kMaxSlots = 32 * kMergeWarps;
 
+// Whether a request of the chunk that the attention kernels took holds token
+// `tok`, by a whole warp, a request a lane: only then were the row's slots
+// written.  (Every request is asked, so that any offsets give what the kernels
+// did; a chunk has several slots a row only with fewer requests than CTAs of a
+// wave or two, so one or a few rounds.)
+__device__ __forceinline__ bool in_chunk(const Args &a, int tok, int lane) {
+  bool mine = false;
+  for (int s = lane; s < a.n_cu; s += 32) {
+    const int t0 = a.cu[s], t1 = a.cu[s + 1];
+    mine |= t0 <= tok && tok < t1 && chunk_ok(a, t0, t1);
+  }
+  return __any_sync(0xffffffffu, mine);
+}
+
 template <int D, typename OutT, int W>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(Args a) {
   pdl_open();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row = W == 1 ? (long long)blockIdx.x * kMergeWarps + warp : (long long)blockIdx.x;
   if (row >= (long long)a.n_tok * a.Hq) return;
-  if (a.cu && a.prefix_lens == nullptr && row / a.Hq >= a.cu[a.n_cu]) return;  // rows behind the last sequence
+  // rows of no request, or of a refused one, stay as they were
+  if (a.cu && a.prefix_lens == nullptr && !in_chunk(a, (int)(row / a.Hq), lane)) return;
   const int S = a.slots, w0 = W == 1 ? 0 : warp;
   const int mine = lane * W + w0;  // this lane's slot
   const float l = mine < S ? __ldcg(a.lse_part + row * S + mine) : -INFINITY;

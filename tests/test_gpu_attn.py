@@ -681,3 +681,57 @@ def test_a_refused_group_gives_its_tails(kv, cu, prefix, max_group, bad):
     o, lse = op(q.cuda(), ints(lens), ints(cu), ints([prefix]))
     A.check(o, lse, A.stack(rows), kv, D, "tails")
     assert qsa_get_device_error()[1] == (4 if bad else 0)
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("window", [40, 2 ** 31 - 1])  # one part a row, and several that are merged
+@pytest.mark.parametrize("cu", [[0, 5, 2], [0, 4, 9], [0, 5, 8], [-1, 2, 4], [2, 4, 8], [0, 4, 6], [4, 8, 0]])
+def test_rows_of_refused_requests_stay_as_they_were(kv, window, cu):
+    Hq, Hkv, D, lens, n, most = 16, 2, 128, [1500, 2000], 8, 4
+    c = A.PagedKV(lens, Hkv, D, kv, 64, "cuda", seed=113)
+    q = queries((n, Hq, D), kv, 114)
+    op = QSAWindowPrefill(c.cache(), 2, n, most, Hq, window)
+    assert (op.ws is None) == (window == 40)
+    garbage(op)
+    op.o.fill_(3.0)
+    op.lse.fill_(5.0)
+    o, lse = op(q.cuda(), ints(cu), ints(lens))
+    live, bad = torch.zeros(n, dtype=torch.bool), False
+    for r, L in enumerate(lens):
+        a, b = cu[r], cu[r + 1]
+        if not (0 <= a <= b <= n and b - a <= most):
+            bad = True
+            continue
+        live[a:b] = True
+        rows = []
+        for j in range(b - a):
+            keys = A.visible(L - (b - a) + j, window, 0)
+            rows.append(A.attend(q[a + j], c.values("k", r, keys), c.values("v", r, keys), D ** -0.5))
+        if rows:
+            A.check(o[a:b], lse[a:b], A.stack(rows), kv, D, "a request beside a refused one")
+    assert (o[~live] == 3).all() and (lse[~live] == 5).all(), "rows of no request changed"
+    assert qsa_get_device_error()[1] == (4 if bad else 0)
+
+
+def test_merged_chunks_of_many_requests():
+    """More requests than the merge asks in one round, some of them refused."""
+    Hq, Hkv, D, B = 2, 1, 64, 70
+    lens = [600 + 7 * r for r in range(B)]
+    c = A.PagedKV(lens, Hkv, D, "bf16", 64, "cuda", seed=115)
+    new = [3 if r % 9 == 4 else r % 3 for r in range(B)]  # at most 2 are taken
+    n = sum(new)
+    q = queries((n, Hq, D), "bf16", 116)
+    op = QSAWindowPrefill(c.cache(), B, n, 2, Hq, 2 ** 31 - 1)
+    assert op.ws is not None
+    garbage(op)
+    op.o.fill_(3.0)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    o, lse = op(q.cuda(), ints(cu), ints(lens))
+    assert qsa_get_device_error()[1] == 4
+    for r, m in enumerate(new):
+        if m > 2:
+            assert (o[cu[r]:cu[r + 1]] == 3).all()
+        elif m:
+            rows = [A.attend(q[cu[r] + j], *(c.values(x, r, range(lens[r] - m + j + 1)) for x in "kv"), D ** -0.5)
+                    for j in range(m)]
+            A.check(o[cu[r]:cu[r + 1]], lse[cu[r]:cu[r + 1]], A.stack(rows), "bf16", D, f"request {r}")
