@@ -15,8 +15,9 @@
 // through the workspace.  fp8 tiles go from shared memory into f16 fragments
 // (fp8_frag.cuh).
 //
-// Weights p = exp(s - max) enter the value product rounded to bf16 (2^-8
-// relative) or, times the V scale, to f16 (2^-11): o is rounded to bf16 itself.
+// Weights p = exp(s - max) enter the value product rounded to bf16 (2^-9
+// relative; o is rounded to bf16 itself) or, times the V scale, to f16 (2^-11, and
+// what f8_ref says about small ones).
 //
 // Measured (B200): batch 32, 16 / 2 heads, window 4,096 + 64 keys, bf16: 27.4 us,
 // 5.0 TB/s (77 % of the measured copy rate; one wave of CTAs starts and ends in
@@ -36,9 +37,10 @@ constexpr int kStageKeys = 16;
 constexpr int kMetaKeys = 128;  // keys whose pages a warp looks up at once: 4 a lane
 
 // Growth of a column's scores (log2) over its reference that is left in the
-// weights (below 2^8, which bf16, f16 and float32 hold as exactly as 1): the
+// weights (bf16: below 2^8, which it holds as exactly as 1; f16: kF8Grow): the
 // lanes then need not agree on a maximum at every stage.
-constexpr float kDecLazy = 8.f;
+template <bool FP8>
+__host__ __device__ constexpr float dec_lazy() { return FP8 ? kF8Grow : 8.f; }
 
 // Stages of a warp's ring: 96 KB (bf16) or 64 KB (fp8) of shared memory a CTA
 // at D = 128, two and three CTAs an SM.
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
     mcol[j][0] = mcol[j][1] = -INFINITY;
     lcol[j][0] = lcol[j][1] = 0.f;
   }
-  float vsref = 0.f;  // power of two that the V scales are relative to
+  float vsref = 0.f;  // power of two that the V scales are relative to (f8_ref)
 
   // fragments of rows 8 j .. 8 j + 7; returns row 8 j + gq's factor on the logits
   auto q_frags = [&](int j, uint32_t(&f)[MD][2]) -> float {
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
           float mx = fabsf(vs_cur);
 #pragma unroll
           for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          const float ref = vs_binade(mx);
+          const float ref = f8_ref(mx);
           if (mx > 0.f && ref > vsref) {
             const float f = vsref / ref;
             vsref = ref;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
             if (!in0) y[j][e] = -INFINITY;
             if (!in1) y[j][2 + e] = -INFINITY;
           }
-          grow |= fmaxf(y[j][e], y[j][2 + e]) > mcol[j][e] + kDecLazy;
+          grow |= fmaxf(y[j][e], y[j][2 + e]) > mcol[j][e] + dec_lazy<FP8>();
         }
       }
       if (__any_sync(0xffffffffu, grow)) {

@@ -25,17 +25,19 @@
 // A step's weights are relative to the maximum of the steps BEFORE it: they
 // need not wait for their own (which runs beside them), and float32 and bf16
 // lose nothing by weights above 1.  When a row's maximum has grown by more than
-// 2^8 the next step starts with rescaling its sum and its output accumulators,
+// 2^8 (f16 weights: 2^4) the next step starts with rescaling its sum and its output accumulators,
 // which stay in tensor memory; the scores of step j are issued behind the values
 // of step j - 1, so the thread that owns the row has them to itself then.  Only
-// growth beyond the weights' range (2^60; f16 weights: 2^13) makes 32 keys start
+// growth beyond the weights' range (2^60; f16 weights: 2^4) makes 32 keys start
 // again with their own maximum.
 //
-// Rounding: weights to bf16, the error of the output's own rounding.  fp8
+// Rounding: weights to bf16, the error of the output's own rounding; where 32 keys
+// start again, the weights of the step's keys before them are rounded once more.  fp8
 // caches run in f16, which holds every E4M3 code: queries scaled per row by a
 // power of two (fp8_frag.cuh says what that keeps), the key scale on the score
 // in float32, and the value scale, relative to a power of two that follows the
-// largest one seen, on the weight before it is rounded to f16 (2^-11).
+// largest one seen, on the weight before it is rounded to f16 (2^-11, and what
+// f8_ref says about small ones).
 //
 // Measured (B200): 8,192 tokens of 32 heads over a window of 8,192 in 0.97 ms
 // (1.13 PFLOP/s, 66 % of the measured cuBLAS burst rate; 1.1 ms repeated, under
@@ -58,7 +60,12 @@ constexpr int kTileLoaders = 4;  // warps
 constexpr int kTileThreads = 16 * 32;
 constexpr int kLoadWarp = 8, kMmaWarp = 12;
 constexpr uint32_t kTmemCols = 512;  // S0, S1 at 0 and 128, O0, O1 at 256 and 384
-constexpr float kLazy = 8.f;    // growth of a row's maximum (log2) that is left in the weights
+// growth (log2) of a row's maximum that is left in the weights of later steps, and of
+// a step's scores that its own weights hold
+template <bool FP8>
+__host__ __device__ constexpr float tile_lazy() { return FP8 ? kF8Grow : 8.f; }
+template <bool FP8>
+__host__ __device__ constexpr float tile_range() { return FP8 ? kF8Grow : 60.f; }
 constexpr unsigned long long kTileWaitNs = 2000000000ull;
 
 template <int D>
@@ -250,7 +257,7 @@ __device__ __forceinline__ void regs_down() {
 
 // What a softmax thread keeps of its row: the maximum (scaled, log2) that sum
 // and outputs are relative to, the sum, the largest score so far, and (fp8) the
-// power of two that the value scales are relative to.
+// power of two that the value scales are relative to (f8_ref).
 struct RowState {
   float mx, l, seen, vref;
 };
@@ -288,14 +295,14 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first
   if (FP8) {
     const float4 w = *reinterpret_cast<const float4 *>(vmax);
     const float v = fmaxf(max3(w.x, w.y, w.z), w.w);
-    if (v > 0.f) ref = fmaxf(ref, dec::vs_binade(v));
+    if (v > 0.f) ref = fmaxf(ref, f8_ref(v));
   }
-  const float late = r.seen > r.mx + kLazy ? r.seen : r.mx;
+  const float late = r.seen > r.mx + tile_lazy<FP8>() ? r.seen : r.mx;
   if (__any_sync(0xffffffffu, late > r.mx || ref > r.vref)) rebase<D, FP8>(r, late, ref, first, o_at);
 
   const f2 sc2 = pack2(scale, scale);
   const float vinv = FP8 && r.vref > 0.f ? 1.f / r.vref : 0.f;
-  constexpr float kRange = FP8 ? 13.f : 60.f;
+  constexpr float kRange = tile_range<FP8>();
   // the scores of keys c .. c + 31, -inf where the row does not see them
   auto scores = [&](int c, uint32_t(&s)[32]) {
     if (FP8) {

@@ -735,3 +735,39 @@ def test_merged_chunks_of_many_requests():
             rows = [A.attend(q[cu[r] + j], *(c.values(x, r, range(lens[r] - m + j + 1)) for x in "kv"), D ** -0.5)
                     for j in range(m)]
             A.check(o[cu[r]:cu[r + 1]], lse[cu[r]:cu[r + 1]], A.stack(rows), "bf16", D, f"request {r}")
+
+
+# ------------------------------------------- small weights of 8-bit caches --
+@pytest.mark.parametrize("form", ["window", "chunk", "prefix"])
+@pytest.mark.parametrize("nats,scales", [(9.0, 0), (12.0, 0), (15.0, 0), (16.1, 0), (17.0, 0), (18.2, 0), (14.0, 5)])
+def test_small_weights_of_an_8_bit_cache(form, nats, scales):
+    """One key far above a flat row (logit + nats) with a value of zero: the
+    output is the others' values times their small weights.  `scales`: that key's
+    page has a V scale 2^scales above the others'.  exp(-18.2) = 2^-26.3 and
+    2^-5 exp(-14) = 2^-25.2 are above 2^-27, to which weights keep 2^-8."""
+    Hq, Hkv, D, page, L = 16, 2, 128, 64, 3001
+    c = A.PagedKV([L], Hkv, D, "e4m3", page, "cuda", seed=121)
+    c.k_scale.fill_(2.0 ** -6)
+    c.v_scale.fill_(2.0 ** -6)
+    c.k.view(torch.uint8).zero_()
+    c.v = (c.v.float().clamp(-200, 200).abs() + 16).to(torch.float8_e4m3fn)
+    top = 70
+    pg = int(c.table_host[0, top // page])
+    c.k[pg, top % page, :, 0] = torch.tensor(256.0).to(torch.float8_e4m3fn)  # times the scale: 4
+    c.v[pg] = torch.tensor(0.0).to(torch.float8_e4m3fn)
+    c.v_scale[pg] *= 2.0 ** scales
+    q = torch.zeros((1, 4, Hq, D), dtype=torch.bfloat16)
+    q[..., 0] = nats * D ** 0.5 / 4
+    dense = 2 ** 31 - 1
+    cache = c.cache()
+    if form == "window":
+        want, _ = window_want(c, q, [L], 4, dense, 0)
+        o, lse = QSAWindowDecode(cache, 1, 4, Hq, dense)(q.cuda(), ints([L]))
+    elif form == "chunk":
+        want, _ = chunk_want(c, q[0], [4], [L], dense, 0)
+        o, lse = QSAWindowPrefill(cache, 1, 4, 4, Hq, dense)(q[0].cuda(), ints([0, 4]), ints([L]))
+    else:
+        want = prefix_want(c, q, [L], 4)
+        o, lse = QSAPrefixDecode(cache, 1, 4, Hq, 1, 1, L - 100, 100)(q.cuda(), ints([L]), ints([0, 1]),
+                                                                     ints([L - 100]))
+    A.check(o, lse, want, "e4m3", D, form)
