@@ -169,7 +169,8 @@ class QSARopeAppend:
         if q.dim() != 3 or q.shape[1] != self.Hq:
             raise ValueError(f"q must be [N, {self.Hq}, D]")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            with torch.cuda.stream(stream):  # its memory belongs to the stream that writes it
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         _rope_append(self._c, self._fn, self.freqs.data_ptr() if self.rotary_dim else None, self.rotary_dim,
                      int(self.interleaved), self.mscale, pos0, cu_new, q, k, v, q_out, stream)
         return q_out

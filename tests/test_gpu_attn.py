@@ -771,3 +771,25 @@ def test_small_weights_of_an_8_bit_cache(form, nats, scales):
         o, lse = QSAPrefixDecode(cache, 1, 4, Hq, 1, 1, L - 100, 100)(q.cuda(), ints([L]), ints([0, 1]),
                                                                      ints([L - 100]))
     A.check(o, lse, want, "e4m3", D, form)
+
+
+# ------------------------------------------------- memory on other streams --
+def test_a_new_q_out_does_not_take_memory_that_the_current_stream_still_reads():
+    """A block freed behind unfinished work of the current stream may be used
+    again on that stream alone: the rows that another stream writes come from
+    that stream's memory."""
+    n, Hq, Hkv, D = 6000, 16, 2, 128  # 24 MB: a block of its own
+    c = A.PagedKV([n], Hkv, D, "bf16", 64, "cuda", seed=131)
+    op = QSARopeAppend(c.cache(), Hq)
+    q, k, v = (queries((n, h, D), "bf16", 132 + h).cuda() for h in (Hq, Hkv, Hkv))
+    pos, cu, side = ints([0]), ints([0, n]), torch.cuda.Stream()
+    want = op(pos, cu, q, k, v)
+    old, copy = torch.ones_like(q), torch.zeros_like(q)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # (clock ticks: some 50 ms)
+    copy.copy_(old)
+    del old
+    got = op(pos, cu, q, k, v, stream=side)
+    torch.cuda.synchronize()
+    assert (copy == 1).all()
+    assert torch.equal(got, want)
