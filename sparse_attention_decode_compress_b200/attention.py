@@ -7,7 +7,9 @@ marshals them, and a class that holds what a serving loop keeps between calls
 the cache's tensors when it is made: their contents may change, the tensors
 may not be replaced.  Its outputs are its own buffers, overwritten by its next
 call.  Work goes to `stream`, by default the current stream of the tensors'
-device.
+device; a handle may be made on one stream and called on others, one at a time,
+and dropped while its last call still runs (on a torch.cuda.ExternalStream only
+after that: torch cannot order memory behind such a stream's work safely).
 """
 from __future__ import annotations
 
@@ -17,7 +19,7 @@ import math
 import torch
 
 from . import _lib
-from .api import QSACache, _check, _need, new_workspace
+from .api import QSACache, _check, _need
 
 _Q_DTYPES = {torch.float32: _lib.QSA_F32, torch.bfloat16: _lib.QSA_BF16}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -38,12 +40,36 @@ class _Caches:
         _, _, self.Hkv, self.D = cache.k_cache.shape
 
 
-def _call(fn, name: str, index: int, args: tuple, stream) -> None:
+class _Buffers:
+    """A handle's own tensors and the streams that have used them: made on the
+    current stream, usable on any."""
+    __slots__ = ("tensors", "seen")
+
+    def __init__(self, c: _Caches, *tensors: torch.Tensor | None):
+        self.tensors = [t for t in tensors if t is not None]
+        made = torch.cuda.current_stream(c.device)
+        self.seen = {made.cuda_stream}
+        # what fills them, and what their memory was used for before on this stream,
+        # ends before another stream may write them (a capture has its own memory)
+        if not torch.cuda.is_current_stream_capturing():
+            made.synchronize()
+
+    def used_on(self, stream: torch.cuda.Stream) -> None:
+        """Keeps their memory, once they are dropped, until `stream` is done."""
+        self.seen.add(stream.cuda_stream)
+        if not isinstance(stream, torch.cuda.ExternalStream):  # (may be gone by then)
+            for t in self.tensors:
+                t.record_stream(stream)
+
+
+def _call(fn, name: str, index: int, args: tuple, stream, buffers: _Buffers | None = None) -> None:
     """fn(*args, stream) with the caches' device as the current one."""
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return _call(fn, name, index, args, stream)
+            return _call(fn, name, index, args, stream, buffers)
     handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    if buffers is not None and handle not in buffers.seen:
+        buffers.used_on(stream if stream is not None else torch.cuda.current_stream(index))
     status = fn(*args, handle)
     if status:
         _check(status, name)
@@ -79,7 +105,7 @@ def _int32(v, name: str) -> int:
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor | None:
-    return new_workspace(nbytes, device) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def _outputs(c: _Caches, shape, o: torch.Tensor, lse: torch.Tensor) -> tuple[int, int]:
@@ -121,7 +147,8 @@ def _rows(t: torch.Tensor, dtype, heads: int, D: int, n: int, name: str, index: 
     return t.data_ptr(), s[0] if n > 1 else heads * D
 
 
-def _rope_append(c: _Caches, fn, freqs, rotary_dim, layout, mscale, pos0, cu_new, q, k, v, q_out, stream):
+def _rope_append(c: _Caches, fn, freqs, rotary_dim, layout, mscale, pos0, cu_new, q, k, v, q_out, stream,
+                 buffers=None):
     n, Hq, _ = q.shape
     B, dt, ix, D = pos0.shape[0], c.dtype, c.index, c.D
     qp, qs = _rows(q, dt, Hq, D, n, "q", ix)
@@ -129,7 +156,7 @@ def _rope_append(c: _Caches, fn, freqs, rotary_dim, layout, mscale, pos0, cu_new
     vp, vs = _rows(v, dt, c.Hkv, D, n, "v", ix)
     _call(fn, "qsa_rope_append", ix,
           (c.ref, B, n, _ints(pos0, B, "pos0", ix), _ints(cu_new, B + 1, "cu_new", ix), qp, qs, kp, ks, vp, vs,
-           c.qd, Hq, freqs, rotary_dim, layout, mscale, _dense(q_out, dt, (n, Hq, D), "q_out", ix)), stream)
+           c.qd, Hq, freqs, rotary_dim, layout, mscale, _dense(q_out, dt, (n, Hq, D), "q_out", ix)), stream, buffers)
 
 
 def qsa_rope_append(cache: QSACache, pos0: torch.Tensor, cu_new: torch.Tensor, q: torch.Tensor,
@@ -164,6 +191,7 @@ class QSARopeAppend:
         self.freqs = torch.tensor([f - (1 << 64) if f >> 63 else f for f in turns], dtype=torch.int64,
                                   device=cache.k_cache.device)
         self._c, self._fn = _Caches(cache), _lib.load().qsa_rope_append
+        self._buffers = _Buffers(self._c, self.freqs)
 
     def __call__(self, pos0, cu_new, q, k, v, q_out=None, stream=None) -> torch.Tensor:
         if q.dim() != 3 or q.shape[1] != self.Hq:
@@ -172,7 +200,7 @@ class QSARopeAppend:
             with torch.cuda.stream(stream):  # its memory belongs to the stream that writes it
                 q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         _rope_append(self._c, self._fn, self.freqs.data_ptr() if self.rotary_dim else None, self.rotary_dim,
-                     int(self.interleaved), self.mscale, pos0, cu_new, q, k, v, q_out, stream)
+                     int(self.interleaved), self.mscale, pos0, cu_new, q, k, v, q_out, stream, self._buffers)
         return q_out
 
 
@@ -211,12 +239,13 @@ class QSAWindowDecode:
         self._head = (c.ref, B, T, Hq)
         self._tail = (self.window, self.sinks, self.sm_scale, *_outputs(c, self._shape, self.o, self.lse),
                       *_bytes(self.ws, c.index))
+        self._buffers = _Buffers(c, self.o, self.lse, self.ws)
 
     def __call__(self, q, ctx_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         c = self._c
         _call(self._fn, "qsa_window_decode", c.index,
               (*self._head, _dense(q, c.dtype, self._shape, "q", c.index), c.qd,
-               _ints(ctx_lens, self._shape[0], "ctx_lens", c.index), *self._tail), stream)
+               _ints(ctx_lens, self._shape[0], "ctx_lens", c.index), *self._tail), stream, self._buffers)
         return self.o, self.lse
 
 
@@ -258,12 +287,13 @@ class QSAWindowPrefill:
         self._head = (c.ref, B, n_tokens, self.max_q)
         self._tail = (c.qd, Hq, self.window, self.sinks, self.sm_scale,
                       *_outputs(c, self._shape, self.o, self.lse), *_bytes(self.ws, c.index))
+        self._buffers = _Buffers(c, self.o, self.lse, self.ws)
 
     def __call__(self, q, cu_q, ctx_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         c = self._c
         _call(self._fn, "qsa_window_prefill", c.index,
               (*self._head, _ints(cu_q, self.B + 1, "cu_q", c.index), _ints(ctx_lens, self.B, "ctx_lens", c.index),
-               _dense(q, c.dtype, self._shape, "q", c.index), *self._tail), stream)
+               _dense(q, c.dtype, self._shape, "q", c.index), *self._tail), stream, self._buffers)
         return self.o, self.lse
 
 
@@ -306,6 +336,7 @@ class QSAPrefixDecode:
         self._head = (c.ref, B, T, Hq)
         self._tail = (*self.bounds, self.sm_scale, *_outputs(c, self._shape, self.o, self.lse),
                       *_bytes(self.ws, c.index))
+        self._buffers = _Buffers(c, self.o, self.lse, self.ws)
 
     def __call__(self, q, ctx_lens, cu_group, prefix_lens, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
         c, n = self._c, self.n_groups
@@ -313,5 +344,5 @@ class QSAPrefixDecode:
               (*self._head, _dense(q, c.dtype, self._shape, "q", c.index), c.qd,
                _ints(ctx_lens, self._shape[0], "ctx_lens", c.index), n,
                _ints(cu_group, n + 1, "cu_group", c.index), _ints(prefix_lens, n, "prefix_lens", c.index),
-               *self._tail), stream)
+               *self._tail), stream, self._buffers)
         return self.o, self.lse

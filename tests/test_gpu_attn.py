@@ -793,3 +793,36 @@ def test_a_new_q_out_does_not_take_memory_that_the_current_stream_still_reads():
     torch.cuda.synchronize()
     assert (copy == 1).all()
     assert torch.equal(got, want)
+
+
+def test_a_handle_made_on_one_stream_is_called_on_another():
+    """The fills of a handle's outputs may not overtake its first call, though
+    the stream that it is made on is late."""
+    L, n, Hq, D = 600, 64, 16, 128
+    c = A.PagedKV([L], 2, D, "bf16", 64, "cuda", seed=133)
+    cache = c.cache()
+    q = queries((n, Hq, D), "bf16", 134)
+    dq, cu, ctx, side = q.cuda(), ints([0, n]), ints([L]), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    o, lse = QSAWindowPrefill(cache, 1, n, n, Hq, 100)(dq, cu, ctx, stream=side)
+    torch.cuda.synchronize()
+    A.check(o, lse, chunk_want(c, q, [n], [L], 100, 0)[0], "bf16", D, "chunk")
+
+
+def test_a_handle_dropped_while_its_call_runs_keeps_its_memory():
+    L, Hq, D = 6000, 16, 128
+    c = A.PagedKV([L], 2, D, "bf16", 64, "cuda", seed=135)
+    q = queries((1, 1, Hq, D), "bf16", 136)
+    dq, ctx, cu, pre, side = q.cuda(), ints([L]), ints([0, 1]), ints([4096]), torch.cuda.Stream()
+    op = QSAPrefixDecode(c.cache(), 1, 1, Hq, 1, 1, 4096, 2000)
+    n = op.ws.numel()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        o, lse = op(dq, ctx, cu, pre)
+    del op
+    others = [torch.full((n,), 1, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((x == 1).all() for x in others)
+    A.check(o, lse, prefix_want(c, q, [L], 1), "bf16", D, "prefix")
