@@ -803,6 +803,7 @@ def test_a_handle_made_on_one_stream_is_called_on_another():
     cache = c.cache()
     q = queries((n, Hq, D), "bf16", 134)
     dq, cu, ctx, side = q.cuda(), ints([0, n]), ints([L]), torch.cuda.Stream()
+    QSAWindowPrefill(cache, 1, n, n, Hq, 100)(dq, cu, ctx)  # (a kernel's first launch may wait for the device)
     torch.cuda.synchronize()
     torch.cuda._sleep(100_000_000)
     o, lse = QSAWindowPrefill(cache, 1, n, n, Hq, 100)(dq, cu, ctx, stream=side)
