@@ -67,8 +67,18 @@ struct Seq {
   bool shared;     // kTail: the prefixes' kernel writes the request's first slots
 };
 
+// A load of what was written before the call; the tails' go to L2 (pdl_begin).
+template <int MODE, typename T>
+__device__ __forceinline__ T ld_mode(const T *p) {
+  if constexpr (MODE == kTail) return __ldcg(p);
+  else return *p;
+}
+
 // Cached tokens of request r; a negative length counts as none.
-__device__ __forceinline__ int ctx_len(const Args &a, int r) { return max(a.ctx_lens[r], 0); }
+template <int MODE>
+__device__ __forceinline__ int ctx_len(const Args &a, int r) {
+  return max(ld_mode<MODE>(a.ctx_lens + r), 0);
+}
 
 // First key in the window of the query at position p.  Positions before 0 (a
 // request with fewer cached tokens than query tokens) count as -1, whose window
@@ -118,25 +128,34 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     }
     q.tok0 = t0;
     q.ntok = t1 - t0;
-    q.first = ctx_len(a, s) - q.ntok;
+    q.first = ctx_len<MODE>(a, s) - q.ntok;
     return q;
   }
   q.tok0 = s * a.T;
   q.ntok = a.T;
-  q.first = ctx_len(a, s) - a.T;
+  q.first = ctx_len<MODE>(a, s) - a.T;
   if (MODE == kTail) {
-    // the group that holds request s: the last one that starts at or before it
-    int lo = 0, hi = a.n_cu;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= s) lo = mid;
-      else hi = mid;
+    // the group that holds request s: the last one that starts at or before it,
+    // by a whole warp, 32 offsets a round (each round waits for L2)
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = a.n_cu;
+    while (n > 32) {
+      const int step = (n + 31) / 32, at = lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, at < n && ld_mode<MODE>(a.cu + lo + min(at, n)) <= s);
+      const int k = m ? 31 - __clz(m) : 0;
+      lo += k * step;
+      n = min(step, n - k * step);
     }
+    const int mine = lo + min(lane, n - 1);
+    const int c0 = ld_mode<MODE>(a.cu + mine), c1 = ld_mode<MODE>(a.cu + mine + 1);
+    const int pre = ld_mode<MODE>(a.prefix_lens + mine);
+    const unsigned m = __ballot_sync(0xffffffffu, lane < n && c0 <= s);
+    const int k = m ? 31 - __clz(m) : 0;
+    const int r0 = __shfl_sync(0xffffffffu, c0, k), r1 = __shfl_sync(0xffffffffu, c1, k);
+    const int prefix = __shfl_sync(0xffffffffu, pre, k);
     // a request outside every group shares nothing, one of a refused group loses
     // its prefix
-    const int r0 = a.cu[lo], r1 = a.cu[lo + 1];
     if (r0 <= s && s < r1) {
-      const int prefix = a.prefix_lens[lo];
       q.prefix = max(prefix, 0);
       q.shared = group_ok(a, r0, r1, prefix);
     }
@@ -156,7 +175,7 @@ __device__ __forceinline__ Seen seen_by(const Args &a, const Seq &q, int i) {
   v.lo = 0;
   if (MODE == kShared) {
     const int tok = q.tok0 + i, r = tok / a.T;
-    v.hi = min(q.prefix, ctx_len(a, r) - a.T + (tok - r * a.T) + 1);
+    v.hi = min(q.prefix, ctx_len<MODE>(a, r) - a.T + (tok - r * a.T) + 1);
     return v;
   }
   v.hi = q.first + i + 1;
@@ -178,11 +197,25 @@ __device__ __forceinline__ bool sees(const Seen &v, int key) {
 // kernel lets it go only behind its own wait (what came before on the stream is
 // then complete for both), and the tails' kernel waits for it at its end, so that
 // the merge, which waits for the tails, waits for both.
+//
+// That earlier work is also VISIBLE to the tails, none of whose threads has waited
+// yet when they read queries, lengths, tables, scales and caches.  The wait makes
+// it visible to the prefixes' kernel, which runs on every SM, so it has reached L2,
+// where all SMs meet; one thread of each of its CTAs then has a gpu-scope fence
+// ahead of its launch_dependents, and the tails start only when all of them have
+// issued that (or ended).  What an SM's L1 may still hold of an earlier call is not
+// asked: the tails' loads go to L2 (ld_mode, cp.async.cg).  That costs a short
+// tail's CTA the latency of its look-ups: 32 requests behind 28,672 keys took 41.3
+// us against 39.5 through L1 (a fence at the start of the tails, which drops the
+// SM's L1, 41.6), 128 behind 250,000 nothing.
 template <int MODE>
 __device__ __forceinline__ void pdl_begin() {
   if (MODE == kShared) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+      __threadfence();
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
   } else if (MODE == kWindow) {
     pdl_open();
   }

@@ -132,12 +132,13 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
                     ((long long)(sq.tok0 + m / a.G) * a.Hq + g * a.G + m % a.G) * D
               : nullptr;
     if constexpr (FP8) {
-      return q_frags_f16<D>(qrow, cq, f) * a.scale_log2;
+      return q_frags_f16<D, MODE == kTail>(qrow, cq, f) * a.scale_log2;
     } else {
 #pragma unroll
       for (int kk = 0; kk < MD; ++kk) {
-        f[kk][0] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq) : 0u;
-        f[kk][1] = qrow ? *reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq + 8) : 0u;
+        const uint32_t *at = reinterpret_cast<const uint32_t *>(qrow + 16 * kk + 2 * cq);
+        f[kk][0] = qrow ? ld_mode<MODE>(at) : 0u;
+        f[kk][1] = qrow ? ld_mode<MODE>(at + 4) : 0u;
       }
       return a.scale_log2;
     }
@@ -170,12 +171,12 @@ __global__ void __launch_bounds__(kDecThreads, NT <= 2 ? 2 : 1) decode_kernel(Ar
       if (x < w1) {
         const int key = rg.key(x);
         const int lp = key / a.c.page_size;
-        const int pg = physical_page(a.c, sq.table, lp);
+        const int pg = physical_page<MODE == kTail>(a.c, sq.table, lp);
         if (pg >= 0) {
           row = (long long)pg * a.c.page_size + (key - lp * a.c.page_size);
           if constexpr (FP8) {
-            ks = a.c.k_scale[(long long)pg * Hkv + g];
-            vs = a.c.v_scale[(long long)pg * Hkv + g];
+            ks = ld_mode<MODE>(a.c.k_scale + (long long)pg * Hkv + g);
+            vs = ld_mode<MODE>(a.c.v_scale + (long long)pg * Hkv + g);
           }
         }
       }

@@ -26,8 +26,9 @@ struct SimpleSmem {
   float v[2][kSimpleKeys][D];
 };
 
+template <int MODE>
 __device__ __forceinline__ float4 load4(const void *p, long long at) {
-  return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+  return ld_mode<MODE>(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at));
 }
 
 // Grid (row tiles, Hkv * splits, sequences).
@@ -58,7 +59,7 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
     if (m < rows) {
       const int row = m0 + m;
       const long long at = ((long long)(sq.tok0 + row / a.G) * a.Hq + g * a.G + row % a.G) * D;
-      v = load4(a.q, at + d);
+      v = load4<MODE>(a.q, at + d);
     }
     *reinterpret_cast<float4 *>(&sm.q[m][d]) = v;
   }
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kSimpleThreads) simple_kernel(Args a) {
     const int x = xt + warp + 4 * lane;
     if (lane >= kOwn || x >= x1) return -1;
     const int key = rg.key(x), lp = key / a.c.page_size;
-    const int pg = physical_page(a.c, sq.table, lp);
+    const int pg = physical_page<MODE == kTail>(a.c, sq.table, lp);
     return pg < 0 ? -1 : (long long)pg * a.c.page_size + (key - lp * a.c.page_size);
   };
   const float *kbase = static_cast<const float *>(a.c.k_cache) + (long long)g * D;

@@ -86,8 +86,9 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 
 // Q B-fragments of one 8-row tile in f16, in the k order above, for query row
 // `qrow` (nullptr: a padding row, all zero).  Returns 2^-e, the factor that
-// takes this row's logits back to Q's scale (lanes of one row agree).
-template <int D>
+// takes this row's logits back to Q's scale (lanes of one row agree).  L2: the
+// row is read past the SM's L1.
+template <int D, bool L2 = false>
 __device__ __forceinline__ float q_frags_f16(const __nv_bfloat16 *qrow, int cq,
                                              uint32_t (&qb)[D / 16][2]) {
   constexpr int MD = D / 16;
@@ -96,11 +97,19 @@ __device__ __forceinline__ float q_frags_f16(const __nv_bfloat16 *qrow, int cq,
 #pragma unroll
   for (int kk = 0; kk < MD; ++kk) {
     const int i = kk >> 2, u = kk & 3;
-    raw[kk] = qrow ? *reinterpret_cast<const uint2 *>(qrow + 16 * (cq + 4 * i) + 4 * u)
-                   : make_uint2(0u, 0u);
+    const __nv_bfloat16 *at = qrow + 16 * (cq + 4 * i) + 4 * u;
+    if (!L2) {
+      raw[kk] = qrow ? *reinterpret_cast<const uint2 *>(at) : make_uint2(0u, 0u);
+    } else if (u % 2 == 0) {  // two k-steps' words: no 32 bytes are asked for again
+      const uint4 w = qrow ? __ldcg(reinterpret_cast<const uint4 *>(at)) : make_uint4(0u, 0u, 0u, 0u);
+      raw[kk] = make_uint2(w.x, w.y);
+      raw[kk + 1] = make_uint2(w.z, w.w);
+    }
+  }
+#pragma unroll
+  for (int kk = 0; kk < MD; ++kk)
     mx = max(mx, max(max(raw[kk].x & 0x7fffu, (raw[kk].x >> 16) & 0x7fffu),
                      max(raw[kk].y & 0x7fffu, (raw[kk].y >> 16) & 0x7fffu)));
-  }
   mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   // bf16 magnitude bits order like the values; biased exponent E:

@@ -113,14 +113,16 @@ struct CacheDev {
 
 // Physical page of logical page `lp` of request r, or -1 (and an error bit)
 // when the logical page lies outside the block table or the entry is not a
-// valid page.
+// valid page.  L2: the entry is read past the SM's L1.
+template <bool L2 = false>
 __device__ __forceinline__ int physical_page(const CacheDev &c, int r, long long lp) {
   if (lp < 0 || lp >= c.max_pages_per_req) {
     record_error(kErrBounds);
     return -1;
   }
   const long long row = c.table_row ? (long long)c.table_row[r] : (long long)r;
-  const int p = c.block_table[row * c.max_pages_per_req + lp];
+  const int32_t *at = c.block_table + row * c.max_pages_per_req + lp;
+  const int p = L2 ? __ldcg(at) : *at;
   if (p < 0 || p >= c.num_pages) {
     record_error(kErrBounds);
     return -1;

@@ -827,3 +827,40 @@ def test_a_handle_dropped_while_its_call_runs_keeps_its_memory():
     torch.cuda.synchronize()
     assert all((x == 1).all() for x in others)
     A.check(o, lse, prefix_want(c, q, [L], 1), "bf16", D, "prefix")
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+def test_the_tails_see_what_was_written_right_before_the_call(kv):
+    """The tails of a shared-prefix decode start beside its prefixes.  Queries,
+    lengths, tails and tables that the work right before the call writes give,
+    step after step without a pause, the bits of steps with a pause between
+    all calls."""
+    Hq, Hkv, D, page, B, P, steps = 16, 2, 128, 16, 6, 64, 60
+    c = A.PagedKV([P + 80] * B, Hkv, D, kv, page, "cuda", seed=141, share={r: (0, P // page) for r in range(1, B)})
+    tables = [torch.from_numpy(c.table_host), torch.from_numpy(c.table_host)]
+    own = tables[1][:, P // page:]
+    tables[1][:, P // page:] = torch.roll(own, 1, 0)  # the tails' pages change hands every step
+    tables = [t.cuda() for t in tables]
+    qkv = [queries((B, Hq + 2 * Hkv, D), kv, 150 + i).cuda() for i in range(steps)]
+    lens = [ints([P + 1 + (7 * r + i) % 79 for r in range(B)]) for i in range(steps)]
+    cu, cug, pl = ints(list(range(B + 1))), ints([0, B]), ints([P])
+
+    def steps_of(pause):
+        cache = c.cache()
+        rope, op = QSARopeAppend(cache, Hq), QSAPrefixDecode(cache, B, 1, Hq, 1, B, P, 80)
+        ctx, pos, outs = ints([0] * B), ints([0] * B), []
+        for i in range(steps):
+            cache.block_table.copy_(tables[i % 2])
+            ctx.copy_(lens[i])
+            torch.sub(ctx, 1, out=pos)
+            pause()
+            x = qkv[i]
+            q = rope(pos, cu, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:])
+            pause()
+            outs.append([t.clone() for t in op(q.view(B, 1, Hq, D), ctx, cug, pl)])
+            pause()
+        torch.cuda.synchronize()
+        return outs
+
+    for a, b in zip(steps_of(torch.cuda.synchronize), steps_of(lambda: None)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
