@@ -58,9 +58,14 @@ AttnPlan plan_stream(long long seqs, int Hkv, long long span, bool merge) {
     if (p.splits > kMaxCluster && span <= 1024LL * kMaxCluster) p.splits = kMaxCluster;
     p.cluster = p.splits > 1 && p.splits <= kMaxCluster;
   } else {
-    // tails of very different lengths: more and smaller pieces (128 tails of 1
-    // to 8,192 keys behind one prefix: 292 us in all against 308 with half as many)
-    p.splits = (int)std::max(1LL, std::min({8LL * kPlanSMs / pairs, ceil_ll(span, 256), 64LL}));
+    // tails of very different lengths: up to eight CTAs an SM (128 tails of 1 to
+    // 8,192 keys behind one prefix: 292 us in all against 308 with half as many),
+    // of 512 keys, but two from 256 keys on.  A CTA begins with a chain of look-ups
+    // in L2: 32 tails of up to 4,096 keys took 36.6 us in all with 512, 41.2 with
+    // 256, 40.9 with 1,024; 8 of up to 8,192 19.1, 27.7 and 18.3; but 64 of up to 512
+    // 32.0 with one piece and 29.6 with two.
+    const long long pieces = std::max(ceil_ll(span, 512), std::min(ceil_ll(span, 256), 2LL));
+    p.splits = (int)std::max(1LL, std::min({8LL * kPlanSMs / pairs, pieces, 64LL}));
   }
   return p;
 }
