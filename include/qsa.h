@@ -590,7 +590,8 @@ qsa_status qsa_window_decode(const qsa_cache *cache, int32_t B, int32_t T, int32
  *   q [n_tokens, Hq, D], o alike, lse [n_tokens, Hq]; Hq / Hkv <= 32
  *   the others as qsa_window_decode
  * BF16 and FP8 caches run on the tensor cores (tcgen05); QSA_ERR_TIMEOUT on the
- * device when one of its bounded waits ran out.
+ * device when one of its bounded waits ran out (the lse of the rows that it left
+ * is NaN then, and where they have parts that are merged their o too).
  */
 size_t qsa_window_prefill_workspace_bytes(const qsa_cache *cache, int32_t B, int32_t n_tokens,
                                           int32_t max_q_per_req, int32_t Hq, int32_t window,

@@ -77,10 +77,17 @@ struct TileSmem {
   // loader's share, and 2^-e of each query row (the row is scaled by 2^e)
   alignas(16) float kscale[4][kTileKeys / 4], vscale[4][kTileKeys / 4], vmax[4][kTileLoaders], qscale[2 * kTileRows];
   alignas(8) uint64_t full[kTileSlots], empty[kTileSlots];
-  uint64_t qfull, sfull[2], pfull[2], ofull[2];
+  uint64_t qfull, sfull[2], pfull[2], ofull[2], drain;
   uint32_t tmem;
   int dead;  // a wait ran out: every role leaves
+  int announced[kTileLoaders];  // tiles that a loader warp has arrived for
 };
+
+template <int D>
+__device__ __forceinline__ TileSmem<D> &tile_smem() {
+  extern __shared__ uint8_t smem_raw[];
+  return *reinterpret_cast<TileSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
 
 __device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
@@ -412,6 +419,32 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first
   tmem_st_wait();
 }
 
+// Ends a CTA of TMA loads, by one warp: if a wait ran out, boxes still in flight
+// land first.  The tiles that the farthest loader warp announced get the arrivals of
+// the others and are waited for, boundedly; that warp had waited for the slot of the
+// tile four ahead, so every warp has announced the tiles before these.  (Out of
+// line, and finding the shared memory again: the kernel has no register for it.)
+template <int D>
+__noinline__ __device__ void land_boxes() {
+  TileSmem<D> &sm = tile_smem<D>();
+  if ((threadIdx.x & 31) != 0 || !*reinterpret_cast<volatile int *>(&sm.dead)) return;
+  int most = 0;
+  for (int w = 0; w < kTileLoaders; ++w) most = max(most, sm.announced[w]);
+  for (int n = max(0, most - kTileSlots); n < most; ++n) {
+    uint64_t *full = &sm.full[n % kTileSlots];
+    for (int w = 0; w < kTileLoaders; ++w)
+      if (sm.announced[w] <= n) mbar_arrive(full);
+    pre::mbar_wait(full, (n / kTileSlots) & 1);
+  }
+}
+// Products in flight, and the arrivals that nobody waits for (the last tiles'
+// slots, or all of them when a wait ran out), end before the CTA and its tensor
+// memory do.
+__noinline__ __device__ void end_products(uint64_t *drain) {
+  pre::umma_commit(drain);
+  pre::mbar_wait(drain, 0);
+}
+
 // The caches as TMA sees them, [token rows][Hkv][D] in boxes of `rows` tokens
 // (0: no TMA) that lie within a page.
 struct TileMaps {
@@ -424,8 +457,7 @@ template <int MODE, int D, bool FP8>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, const __grid_constant__ TileMaps maps) {
   pdl_begin<MODE>();
   using SM = TileSmem<D>;
-  extern __shared__ uint8_t smem_raw[];
-  SM &sm = *reinterpret_cast<SM *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  SM &sm = tile_smem<D>();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Seq sq = sequence<MODE>(a, blockIdx.z);
   // the last tiles of a causal chunk see the most keys: they go first
@@ -447,13 +479,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    // bf16: every loader thread's copies; fp8: every loader warp
-    constexpr uint32_t kArrivals = kTileLoaders;
+    // each of the four loader warps arrives once for a tile (its boxes by TMA with
+    // the bytes they bring, its own copies when they stand)
     for (int i = 0; i < kTileSlots; ++i) {
-      mbar_init(&sm.full[i], kArrivals);
+      mbar_init(&sm.full[i], kTileLoaders);
       mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.qfull, kLoadWarp);
+    mbar_init(&sm.drain, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.sfull[t], 1);
       mbar_init(&sm.pfull[t], 4);
@@ -636,6 +669,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
             }
           }
         }
+      } else if (live) {  // a wait ran out: no result passes for one
+        (a.slots > 1 ? a.lse_part[slot] : a.lse[at]) = NAN;
       }
     }
   } else if (warp >= kMmaWarp) {
@@ -697,6 +732,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
           pre::fence_async_smem();
         }
       }
+      end_products(&sm.drain);
     }
     __syncwarp();
   } else {
@@ -793,7 +829,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
     if constexpr (!FP8) {
       // tile n of the ring: keys (n even) or values (n odd) of step n / 2
       int behind = -1;  // slot whose copies by this warp are not announced yet
-      for (int n = 0; n < 2 * nt; ++n) {
+      int n = 0;
+      for (; n < 2 * nt; ++n) {
         const int j = n >> 1, slot = n % kTileSlots;
         if (n >= 2 && (n & 1) == 0) {
           place(j, pg_next, in_next);
@@ -838,6 +875,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
       cp_async_wait<0>();
       __syncwarp();
       if (lane == 0 && behind >= 0) mbar_arrive(&sm.full[behind]);
+      if (lane == 0) sm.announced[wl] = n;
     } else {
       // fp8: raw rows of the next tile are loaded while this one is converted
       uint4 raw[2][kLoads];
@@ -902,6 +940,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const Args a, con
   pre::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
+    if (!FP8) land_boxes<D>();
+    __syncwarp();
     pre::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
