@@ -27,10 +27,15 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 class _Caches:
     """What every call takes from the caches, found once: the C struct (and a
-    reference to it), the device index, the query type and the head shape."""
-    __slots__ = ("struct", "ref", "index", "dtype", "qd", "Hkv", "D", "device")
+    reference to it), the device index, the query type, the head shape and the
+    requests that the block table has rows for (B: those of a call or handle)."""
+    __slots__ = ("struct", "ref", "index", "dtype", "qd", "Hkv", "D", "device", "rows")
 
-    def __init__(self, cache: QSACache):
+    def __init__(self, cache: QSACache, B: int = 0):
+        if cache.block_table.dim() != 2:
+            raise ValueError("block_table must be [requests, pages]")
+        self.rows = cache.block_table.shape[0]
+        self.holds(B)
         self.struct = cache.struct()
         self.ref = ctypes.byref(self.struct)
         self.device = cache.k_cache.device
@@ -38,6 +43,10 @@ class _Caches:
         self.dtype = torch.float32 if cache.k_cache.dtype == torch.float32 else torch.bfloat16
         self.qd = _Q_DTYPES[self.dtype]
         _, _, self.Hkv, self.D = cache.k_cache.shape
+
+    def holds(self, B: int) -> None:
+        if B > self.rows:
+            raise ValueError(f"block_table has {self.rows} rows for {B} requests")
 
 
 class _Buffers:
@@ -151,6 +160,7 @@ def _rope_append(c: _Caches, fn, freqs, rotary_dim, layout, mscale, pos0, cu_new
                  buffers=None):
     n, Hq, _ = q.shape
     B, dt, ix, D = pos0.shape[0], c.dtype, c.index, c.D
+    c.holds(B)
     qp, qs = _rows(q, dt, Hq, D, n, "q", ix)
     kp, ks = _rows(k, dt, c.Hkv, D, n, "k", ix)
     vp, vs = _rows(v, dt, c.Hkv, D, n, "v", ix)
@@ -214,9 +224,9 @@ def qsa_window_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
                       stream=None) -> None:
     """Decode attention of q [B, T, Hq, D] over each request's last `window`
     keys and first `sinks` keys.  o: q's type and shape, lse float32."""
-    c = _Caches(cache)
-    _heads(q, c)
     B, T, Hq, _ = shape = q.shape
+    c = _Caches(cache, B)
+    _heads(q, c)
     ix = c.index
     _call(_lib.load().qsa_window_decode, "qsa_window_decode", ix,
           (c.ref, B, T, Hq, _dense(q, c.dtype, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix),
@@ -230,7 +240,7 @@ class QSAWindowDecode:
     def __init__(self, cache: QSACache, B: int, T: int, Hq: int, window: int, sinks: int = 0,
                  sm_scale: float | None = None):
         self.cache, self.window, self.sinks = cache, _int32(window, "window"), _int32(sinks, "sinks")
-        c = self._c = _Caches(cache)
+        c = self._c = _Caches(cache, B)
         self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
         self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)
         self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=c.device)
@@ -260,10 +270,11 @@ def qsa_window_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tens
                        lse: torch.Tensor, workspace: torch.Tensor | None, stream=None) -> None:
     """Window attention of a prefill chunk: rows cu_q[r] .. cu_q[r+1]-1 of q
     [N, Hq, D] are the newest tokens of request r."""
-    c = _Caches(cache)
-    _heads(q, c)
     n, Hq, _ = shape = q.shape
-    B, ix = ctx_lens.shape[0], c.index
+    B = ctx_lens.shape[0]
+    c = _Caches(cache, B)
+    _heads(q, c)
+    ix = c.index
     _call(_lib.load().qsa_window_prefill, "qsa_window_prefill", ix,
           (c.ref, B, n, _int32(max_q_per_req, "max_q_per_req"), _ints(cu_q, B + 1, "cu_q", ix),
            _ints(ctx_lens, B, "ctx_lens", ix), _dense(q, c.dtype, shape, "q", ix), c.qd, Hq, _int32(window, "window"),
@@ -277,7 +288,7 @@ class QSAWindowPrefill:
                  sinks: int = 0, sm_scale: float | None = None):
         self.cache, self.window, self.sinks = cache, _int32(window, "window"), _int32(sinks, "sinks")
         self.B, self.max_q = B, _int32(max_q_per_req, "max_q_per_req")
-        c = self._c = _Caches(cache)
+        c = self._c = _Caches(cache, B)
         self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
         self.o = torch.zeros((n_tokens, Hq, c.D), dtype=c.dtype, device=c.device)
         self.lse = torch.full((n_tokens, Hq), -math.inf, dtype=torch.float32, device=c.device)
@@ -309,9 +320,9 @@ def qsa_prefix_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, 
                       o: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """Decode attention of q [B, T, Hq, D] where the requests of a group share
     their first prefix_lens[g] keys."""
-    c = _Caches(cache)
-    _heads(q, c)
     B, T, Hq, _ = shape = q.shape
+    c = _Caches(cache, B)
+    _heads(q, c)
     n, ix = prefix_lens.shape[0], c.index
     _call(_lib.load().qsa_prefix_decode, "qsa_prefix_decode", ix,
           (c.ref, B, T, Hq, _dense(q, c.dtype, shape, "q", ix), c.qd, _ints(ctx_lens, B, "ctx_lens", ix), n,
@@ -327,7 +338,7 @@ class QSAPrefixDecode:
                  max_tail: int, sm_scale: float | None = None):
         self.cache, self.n_groups = cache, n_groups
         self.bounds = tuple(_int32(v, "a bound") for v in (max_group, max_prefix, max_tail))
-        c = self._c = _Caches(cache)
+        c = self._c = _Caches(cache, B)
         self.sm_scale = 1.0 / math.sqrt(c.D) if sm_scale is None else float(sm_scale)
         self.o = torch.empty((B, T, Hq, c.D), dtype=c.dtype, device=c.device)
         self.lse = torch.empty((B, T, Hq), dtype=torch.float32, device=c.device)

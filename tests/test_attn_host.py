@@ -204,3 +204,38 @@ def test_binding_refuses_what_does_not_fit_32_bits(v):
                  lambda: QSAWindowPrefill(c, 2, 8, v, 4, 16), lambda: QSAPrefixDecode(c, 2, 1, 4, 1, 1, v, 1)):
         with pytest.raises(ValueError, match="32 bits"):
             make()
+
+
+def host_cache(rows=2, kv=torch.bfloat16, **kw):
+    from sparse_attention_decode_compress_b200 import QSACache
+    k = torch.zeros((4, 16, 2, 64)).to(kv)
+    c = QSACache.allocate(k, k.clone(), torch.zeros((rows, 2), dtype=torch.int32), 32, rows)
+    for name, v in kw.items():
+        setattr(c, name, v)
+    return c
+
+
+def all_calls(c, B):
+    """Every call of the module on cache c for B requests (host tensors: the
+    shapes are looked at before the devices)."""
+    import sparse_attention_decode_compress_b200 as qsa
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    dt = torch.float32 if c.k_cache.dtype == torch.float32 else torch.bfloat16
+    q, o, lse = (torch.zeros(s, dtype=t) for s, t in (((B, 1, 4, 64), dt), ((B, 1, 4, 64), dt),
+                                                      ((B, 1, 4), torch.float32)))
+    r, ro, rl = q[:, 0], o[:, 0], lse[:, 0]
+    return [lambda: qsa.QSAWindowDecode(c, B, 1, 4, 16), lambda: qsa.QSAWindowPrefill(c, B, B, 1, 4, 16),
+            lambda: qsa.QSAPrefixDecode(c, B, 1, 4, 1, 1, 16, 16),
+            lambda: qsa.qsa_window_decode(c, q, i32(B), 16, 0, 1.0, o, lse, None),
+            lambda: qsa.qsa_window_prefill(c, i32(B + 1), i32(B), 1, r, 16, 0, 1.0, ro, rl, None),
+            lambda: qsa.qsa_prefix_decode(c, q, i32(B), i32(2), i32(1), 1, 16, 16, 1.0, o, lse, None)]
+
+
+def test_more_requests_than_the_block_table_has_rows():
+    """(the kernels would read behind the table)"""
+    for call in all_calls(host_cache(rows=2), 3):
+        with pytest.raises(ValueError, match="2 rows for 3 requests"):
+            call()
+    for call in all_calls(host_cache(block_table=torch.zeros(8, dtype=torch.int32)), 2):
+        with pytest.raises(ValueError, match=r"\[requests, pages\]"):
+            call()

@@ -864,3 +864,14 @@ def test_the_tails_see_what_was_written_right_before_the_call(kv):
 
     for a, b in zip(steps_of(torch.cuda.synchronize), steps_of(lambda: None)):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------------------- the binding --
+def test_no_call_takes_more_requests_than_the_block_table_has_rows():
+    c = A.PagedKV([40, 40], 2, 64, "bf16", 16, "cuda", seed=151)
+    cache, q = c.cache(), queries((3, 1, 4, 64), "bf16", 152).cuda()
+    for make in (lambda: QSAWindowDecode(cache, 3, 1, 4, 16), lambda: QSAWindowPrefill(cache, 3, 3, 1, 4, 16),
+                 lambda: QSAPrefixDecode(cache, 3, 1, 4, 1, 1, 16, 16),
+                 lambda: QSARopeAppend(cache, 4)(ints([0] * 3), ints([0, 1, 2, 3]), q[:, 0], q[:, 0, :2], q[:, 0, :2])):
+        with pytest.raises(ValueError, match="2 rows for 3 requests"):
+            make()
