@@ -36,6 +36,14 @@ class _Caches:
             raise ValueError("block_table must be [requests, pages]")
         self.rows = cache.block_table.shape[0]
         self.holds(B)
+        k, at = cache.k_cache, cache.k_cache.get_device()
+        if k.dtype == torch.float8_e4m3fn:
+            for t, name in ((cache.k_scale, "k_scale"), (cache.v_scale, "v_scale")):
+                if t is None or t.dtype is not torch.float32 or t.shape != (k.shape[0], k.shape[2]):
+                    raise ValueError(f"{name} of an 8-bit cache must be float32 [{k.shape[0]}, {k.shape[2]}]")
+        for t in (cache.v_cache, cache.block_table, cache.k_scale, cache.v_scale):
+            if t is not None and t.get_device() != at:
+                raise ValueError("the cache's tensors are on different devices")
         self.struct = cache.struct()
         self.ref = ctypes.byref(self.struct)
         self.device = cache.k_cache.device

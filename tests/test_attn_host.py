@@ -239,3 +239,17 @@ def test_more_requests_than_the_block_table_has_rows():
     for call in all_calls(host_cache(block_table=torch.zeros(8, dtype=torch.int32)), 2):
         with pytest.raises(ValueError, match=r"\[requests, pages\]"):
             call()
+
+
+def test_scales_of_8_bit_caches():
+    """(a short or differently typed scale would be read behind its end)"""
+    f8, good = torch.float8_e4m3fn, torch.ones(4, 2)
+    for bad in (None, good.to(torch.bfloat16), good.double(), torch.ones(8), torch.ones(3, 2), torch.ones(2, 4)):
+        for kw in (dict(k_scale=bad, v_scale=good), dict(k_scale=good, v_scale=bad)):
+            for call in all_calls(host_cache(kv=f8, **kw), 2):
+                with pytest.raises(ValueError, match=r"8-bit cache must be float32 \[4, 2\]"):
+                    call()
+    # the host caches above are refused for being on the host, and for nothing before
+    for call in all_calls(host_cache(kv=f8, k_scale=good, v_scale=good), 2) + all_calls(host_cache(), 2):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call()
