@@ -4,8 +4,8 @@ append, window attention (decode and prefill) and shared-prefix decode.
 Each C entry point has a function of its name, which checks its arguments and
 marshals them, and a class that holds what a serving loop keeps between calls
 (the cache description, the output buffers and the workspace).  A class takes
-the cache's tensors when it is made: their contents may change, the tensors
-may not be replaced.  Its outputs are its own buffers, overwritten by its next
+the cache's tensors when it is made and keeps them: their contents may change; a
+tensor put in the place of one later is not seen.  Its outputs are its own buffers, overwritten by its next
 call.  Work goes to `stream`, by default the current stream of the tensors'
 device; a handle may be made on one stream and called on others, one at a time,
 and dropped while its last call still runs (on a torch.cuda.ExternalStream only
@@ -29,7 +29,7 @@ class _Caches:
     """What every call takes from the caches, found once: the C struct (and a
     reference to it), the device index, the query type, the head shape and the
     requests that the block table has rows for (B: those of a call or handle)."""
-    __slots__ = ("struct", "ref", "index", "dtype", "qd", "Hkv", "D", "device", "rows")
+    __slots__ = ("struct", "ref", "index", "dtype", "qd", "Hkv", "D", "device", "rows", "tensors")
 
     def __init__(self, cache: QSACache, B: int = 0):
         if cache.block_table.dim() != 2:
@@ -45,6 +45,8 @@ class _Caches:
             if t is not None and t.get_device() != at:
                 raise ValueError("the cache's tensors are on different devices")
         self.struct = cache.struct()
+        # the struct holds their addresses: they live as long as it does
+        self.tensors = (cache.k_cache, cache.v_cache, cache.block_table, cache.k_scale, cache.v_scale)
         self.ref = ctypes.byref(self.struct)
         self.device = cache.k_cache.device
         self.index = cache.k_cache.get_device()

@@ -875,3 +875,20 @@ def test_no_call_takes_more_requests_than_the_block_table_has_rows():
                  lambda: QSARopeAppend(cache, 4)(ints([0] * 3), ints([0, 1, 2, 3]), q[:, 0], q[:, 0, :2], q[:, 0, :2])):
         with pytest.raises(ValueError, match="2 rows for 3 requests"):
             make()
+
+
+def test_a_handle_keeps_the_tensors_it_was_made_with():
+    c = A.PagedKV([300, 200], 2, 128, "e4m3", 16, "cuda", seed=153)
+    cache = c.cache()
+    old = [cache.k_cache, cache.v_cache, cache.block_table, cache.k_scale, cache.v_scale]
+    addresses = {t.data_ptr() for t in old}
+    op = QSAWindowDecode(cache, 2, 1, 16, 100)
+    for name in ("k_cache", "v_cache", "block_table", "k_scale", "v_scale"):
+        setattr(cache, name, getattr(cache, name).clone())
+    shapes = [(t.shape, t.dtype) for t in old]
+    del old, c.dk, c.dv
+    new = [torch.zeros(s, dtype=torch.uint8, device="cuda").to(d) for s, d in shapes for _ in range(4)]
+    assert not addresses & {t.data_ptr() for t in new}, "memory that the handle reads was given away"
+    q = queries((2, 1, 16, 128), "e4m3", 154)
+    o, lse = op(q.cuda(), ints([300, 200]))
+    A.check(o, lse, window_want(c, q, [300, 200], 1, 100, 0)[0], "e4m3", 128, "window")
