@@ -123,6 +123,10 @@ def _int32(v, name: str) -> int:
     return v
 
 
+def _sizes(*v) -> tuple[int, ...]:
+    return tuple(_int32(x, "a size") for x in v)
+
+
 def _workspace(nbytes: int, device) -> torch.Tensor | None:
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
@@ -145,10 +149,12 @@ def qsa_rope_freqs(rotary_dim: int, theta: float = 10000.0, scaling: str = "none
     of 2^-64, their radians per token, and the factor on the rotated dims."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
-    n = max(int(rotary_dim), 0) // 2
+    rotary_dim = _int32(rotary_dim, "rotary_dim")
+    original_max_position = _int32(original_max_position, "original_max_position")
+    n = min(max(rotary_dim, 0), 128) // 2  # (above 128: refused)
     fr, inv, m = (ctypes.c_uint64 * max(n, 1))(), (ctypes.c_double * max(n, 1))(), ctypes.c_float()
-    _check(_lib.load().qsa_rope_freqs(int(rotary_dim), float(theta), _SCALINGS[scaling], float(factor),
-                                      int(original_max_position), float(beta_fast), float(beta_slow),
+    _check(_lib.load().qsa_rope_freqs(rotary_dim, float(theta), _SCALINGS[scaling], float(factor),
+                                      original_max_position, float(beta_fast), float(beta_slow),
                                       ctypes.addressof(inv), ctypes.addressof(fr), ctypes.byref(m)),
            "qsa_rope_freqs")
     return list(fr[:n]), list(inv[:n]), m.value
@@ -186,7 +192,7 @@ def qsa_rope_append(cache: QSACache, pos0: torch.Tensor, cu_new: torch.Tensor, q
     pages, and copies v there.  `freqs`: int64 [rotary_dim / 2] on the cache's
     device, the bits of qsa_rope_freqs.  q, k, v may be strided over tokens
     (parts of one fused projection)."""
-    rotary_dim = int(rotary_dim)
+    rotary_dim = _int32(rotary_dim, "rotary_dim")
     c = _Caches(cache)
     _need(freqs, torch.int64, "freqs")
     if freqs.shape != (max(rotary_dim, 0) // 2,) or freqs.get_device() != c.index or not freqs.is_contiguous():
@@ -226,7 +232,8 @@ class QSARopeAppend:
 
 # ----------------------------------------------------------------- window --
 def qsa_window_decode_workspace_bytes(cache: QSACache, B: int, T: int, Hq: int, window: int, sinks: int) -> int:
-    return int(_lib.load().qsa_window_decode_workspace_bytes(ctypes.byref(cache.struct()), B, T, Hq, window, sinks))
+    return int(_lib.load().qsa_window_decode_workspace_bytes(ctypes.byref(cache.struct()),
+                                                             *_sizes(B, T, Hq, window, sinks)))
 
 
 def qsa_window_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, window: int, sinks: int,
@@ -271,8 +278,8 @@ class QSAWindowDecode:
 
 def qsa_window_prefill_workspace_bytes(cache: QSACache, B: int, n_tokens: int, max_q_per_req: int, Hq: int,
                                        window: int, sinks: int) -> int:
-    return int(_lib.load().qsa_window_prefill_workspace_bytes(ctypes.byref(cache.struct()), B, n_tokens,
-                                                              max_q_per_req, Hq, window, sinks))
+    return int(_lib.load().qsa_window_prefill_workspace_bytes(ctypes.byref(cache.struct()),
+                                                              *_sizes(B, n_tokens, max_q_per_req, Hq, window, sinks)))
 
 
 def qsa_window_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tensor, max_q_per_req: int,
@@ -321,8 +328,9 @@ class QSAWindowPrefill:
 # ----------------------------------------------------------------- prefix --
 def qsa_prefix_decode_workspace_bytes(cache: QSACache, B: int, T: int, Hq: int, n_groups: int, max_group: int,
                                       max_prefix: int, max_tail: int) -> int:
-    return int(_lib.load().qsa_prefix_decode_workspace_bytes(ctypes.byref(cache.struct()), B, T, Hq, n_groups,
-                                                             max_group, max_prefix, max_tail))
+    return int(_lib.load().qsa_prefix_decode_workspace_bytes(ctypes.byref(cache.struct()),
+                                                             *_sizes(B, T, Hq, n_groups, max_group, max_prefix,
+                                                                     max_tail)))
 
 
 def qsa_prefix_decode(cache: QSACache, q: torch.Tensor, ctx_lens: torch.Tensor, cu_group: torch.Tensor,

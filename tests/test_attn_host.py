@@ -253,3 +253,23 @@ def test_scales_of_8_bit_caches():
     for call in all_calls(host_cache(kv=f8, k_scale=good, v_scale=good), 2) + all_calls(host_cache(), 2):
         with pytest.raises(ValueError, match="CUDA tensors"):
             call()
+
+
+@pytest.mark.parametrize("v", [1 << 31, (1 << 32) + 64, -(1 << 31) - 1])
+def test_frequencies_and_workspaces_refuse_what_does_not_fit_32_bits(v):
+    import sparse_attention_decode_compress_b200 as qsa
+    with pytest.raises(ValueError, match="32 bits"):
+        qsa_rope_freqs(v)
+    with pytest.raises(ValueError, match="32 bits"):
+        qsa_rope_freqs(64, scaling="yarn", factor=2.0, original_max_position=v)
+
+    class Described:  # the workspace calls read a cache's geometry alone
+        def struct(self):
+            return cache()._obj
+
+    for fn, n in ((qsa.qsa_window_decode_workspace_bytes, 5), (qsa.qsa_window_prefill_workspace_bytes, 6),
+                  (qsa.qsa_prefix_decode_workspace_bytes, 7)):
+        fn(Described(), *[2] * n)
+        for i in range(n):
+            with pytest.raises(ValueError, match="32 bits"):
+                fn(Described(), *[v if j == i else 2 for j in range(n)])
