@@ -55,11 +55,12 @@ def _need(t: torch.Tensor, dtype, name: str):
 class QSACache:
     """One attention layer's paged caches (a single cache group: the same
     block-table entry names the same physical page in K, V and the
-    compressed-key cache)."""
+    compressed-key cache).  A layer without an indexer has neither kc nor ring
+    (both None): the calls that read or write them are refused."""
     k_cache: torch.Tensor               # [num_pages, P, Hkv, D] f32 / bf16 / fp8 e4m3
     v_cache: torch.Tensor
-    kc: torch.Tensor                    # uint8 [num_pages, qsa_kc_page_bytes(P, d)], packed
-    ring: torch.Tensor                  # int8 [ring_rows, 4, d]
+    kc: torch.Tensor | None             # uint8 [num_pages, qsa_kc_page_bytes(P, d)], packed
+    ring: torch.Tensor | None           # int8 [ring_rows, 4, d]
     block_table: torch.Tensor           # int32 [B, max_pages]
     k_scale: torch.Tensor | None = None  # f32 [num_pages, Hkv] (fp8 only)
     v_scale: torch.Tensor | None = None
@@ -67,6 +68,9 @@ class QSACache:
     @staticmethod
     def allocate(k_cache, v_cache, block_table, idx_dim: int, ring_rows: int,
                  k_scale=None, v_scale=None) -> "QSACache":
+        """idx_dim 0: no compressed keys and no ring."""
+        if idx_dim == 0:
+            return QSACache(k_cache, v_cache, None, None, block_table, k_scale, v_scale)
         num_pages, P = k_cache.shape[0], k_cache.shape[1]
         page_bytes = int(_lib.load().qsa_kc_page_bytes(P, idx_dim))
         if page_bytes == 0:
@@ -75,27 +79,37 @@ class QSACache:
         ring = torch.zeros((ring_rows, 4, idx_dim), dtype=torch.int8, device=k_cache.device)
         return QSACache(k_cache, v_cache, kc, ring, block_table, k_scale, v_scale)
 
+    @property
+    def idx_dim(self) -> int:
+        if self.ring is None:
+            raise ValueError("this cache has no compressed keys (idx_dim 0)")
+        return self.ring.shape[-1]
+
     def struct(self) -> _lib.QsaCacheStruct:
         k, v = self.k_cache, self.v_cache
         if k.dtype not in _KV_DTYPES or v.dtype != k.dtype or k.shape != v.shape or k.dim() != 4:
             raise TypeError("k_cache / v_cache must be [num_pages, P, Hkv, D] of one dtype "
                             "(float32, bfloat16 or float8_e4m3fn)")
-        _need(self.kc, torch.uint8, "kc")
-        _need(self.ring, torch.int8, "ring")
         _need(self.block_table, torch.int32, "block_table")
         num_pages, P, Hkv, D = k.shape
-        d = self.ring.shape[-1]
-        page_bytes = int(_lib.load().qsa_kc_page_bytes(P, d))
-        if self.ring.dim() != 3 or self.ring.shape[1] != 4 or page_bytes == 0 or \
-                self.kc.shape != (num_pages, page_bytes):
-            raise ValueError("ring must be [rows, 4, d] and kc [num_pages, qsa_kc_page_bytes(P, d)]")
+        d = 0
+        if self.kc is not None or self.ring is not None:
+            if self.kc is None or self.ring is None:
+                raise ValueError("kc and ring belong together: both or neither")
+            _need(self.kc, torch.uint8, "kc")
+            _need(self.ring, torch.int8, "ring")
+            d = self.ring.shape[-1]
+            page_bytes = int(_lib.load().qsa_kc_page_bytes(P, d))
+            if self.ring.dim() != 3 or self.ring.shape[1] != 4 or page_bytes == 0 or \
+                    self.kc.shape != (num_pages, page_bytes):
+                raise ValueError("ring must be [rows, 4, d] and kc [num_pages, qsa_kc_page_bytes(P, d)]")
         s = _lib.QsaCacheStruct()
         s.num_pages, s.page_size, s.num_kv_heads, s.head_dim, s.idx_dim = num_pages, P, Hkv, D, d
         s.kv_dtype = _KV_DTYPES[k.dtype]
         s.k_cache, s.v_cache = _ptr(k), _ptr(v)
         s.k_scale, s.v_scale = _ptr(self.k_scale), _ptr(self.v_scale)
         s.kc, s.ring = _ptr(self.kc), _ptr(self.ring)
-        s.ring_rows = self.ring.shape[0]
+        s.ring_rows = 0 if self.ring is None else self.ring.shape[0]
         s.block_table = _ptr(self.block_table)
         s.max_pages_per_req = self.block_table.shape[1]
         return s
@@ -310,7 +324,7 @@ def allocate_norm_caches(cache: QSACache, ring_rows: int) -> tuple[torch.Tensor,
     `cache` (its block table names their pages): float16 compressed keys
     [num_pages, P/4, d] and the bfloat16 raw-key ring [ring_rows, 4, d]."""
     num_pages, P = cache.k_cache.shape[0], cache.k_cache.shape[1]
-    d = cache.ring.shape[-1]
+    d = cache.idx_dim
     if qsa_kcn_page_bytes(P, d) == 0:
         raise ValueError(f"unsupported compressed-key geometry: page_size {P}, idx_dim {d}")
     dev = cache.k_cache.device
@@ -321,7 +335,7 @@ def allocate_norm_caches(cache: QSACache, ring_rows: int) -> tuple[torch.Tensor,
 
 def _check_norm_caches(cache: QSACache, kcn: torch.Tensor, ring: torch.Tensor):
     num_pages, P = cache.k_cache.shape[0], cache.k_cache.shape[1]
-    d = cache.ring.shape[-1]
+    d = cache.idx_dim
     _need(kcn, torch.float16, "kcn")
     _need(ring, torch.bfloat16, "ring")
     if tuple(kcn.shape) != (num_pages, P // 4, d) or ring.dim() != 3 or ring.shape[1:] != (4, d):
@@ -405,7 +419,7 @@ def qsa_sparse_prefill(cache: QSACache, cu_q: torch.Tensor, ctx_lens: torch.Tens
     _need(o, torch.float32, "o")
     _need(lse, torch.float32, "lse")
     B = ctx_lens.shape[0]
-    d = cache.ring.shape[-1]
+    d = cache.idx_dim
     if cu_q.shape[0] != B + 1 or q_idx.shape != (Nq, d) or k_chunk.shape != (Nq, d):
         raise ValueError("cu_q [B+1], q_idx and k_chunk [Nq, d] expected")
     if sel.shape != (Nq, topk) or o.shape != (Nq, Hq, D) or lse.shape != (Nq, Hq):
@@ -433,7 +447,7 @@ class QSASession:
         self._struct = cache.struct()
         self.B, self.T, self.Hq, self.topk = B, T, Hq, topk
         self.D = cache.k_cache.shape[-1]
-        self.d = cache.ring.shape[-1]
+        self.d = cache.idx_dim
         self.q_dtype = q_dtype
         qd = {torch.float32: _lib.QSA_F32, torch.bfloat16: _lib.QSA_BF16}[q_dtype]
         lib = _lib.load()

@@ -273,3 +273,31 @@ def test_frequencies_and_workspaces_refuse_what_does_not_fit_32_bits(v):
         for i in range(n):
             with pytest.raises(ValueError, match="32 bits"):
                 fn(Described(), *[v if j == i else 2 for j in range(n)])
+
+
+# ------------------------------------------------- layers without an index --
+def test_a_cache_without_an_index():
+    """What reads neither compressed keys nor the ring needs none of them; what
+    does is refused."""
+    from sparse_attention_decode_compress_b200 import (QSACache, QSASession, allocate_norm_caches,
+                                                       qsa_sparse_prefill)
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    c = QSACache.allocate(k, k.clone(), torch.zeros((2, 2), dtype=torch.int32), 0, 0)
+    assert c.kc is None and c.ring is None
+    for call in all_calls(c, 2):  # refused for being on the host alone
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call()
+    q, i = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: allocate_norm_caches(c, 2),
+                 lambda: qsa_sparse_prefill(c, i, i[:2], 1, q[:, 0].to(torch.int8), q[:, 0].to(torch.int8), q, 4, 4, 1.0,
+                                            torch.zeros((2, 4), dtype=torch.int32), q.float(), q[..., 0].float(), q)):
+        with pytest.raises(ValueError, match="no compressed keys"):
+            call()
+    half = QSACache(k, k.clone(), None, torch.zeros((2, 4, 32), dtype=torch.int8), c.block_table)
+    with pytest.raises(ValueError, match="both or neither"):
+        half.struct()
+    # the C entries refuse the struct of such a cache
+    lib, s = _lib.load(), cache()
+    assert lib.qsa_compress_append(s, 2, P, P, P, 1, None) == INVALID
+    assert lib.qsa_index_topk(s, 2, P, P, None, 4, 4, P, None, P, 1 << 30, None) == INVALID
+    assert lib.qsa_index_topk_noalloc(s, 2, P, P, None, 4, 4, P, None) == INVALID

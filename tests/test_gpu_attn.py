@@ -892,3 +892,28 @@ def test_a_handle_keeps_the_tensors_it_was_made_with():
     q = queries((2, 1, 16, 128), "e4m3", 154)
     o, lse = op(q.cuda(), ints([300, 200]))
     A.check(o, lse, window_want(c, q, [300, 200], 1, 100, 0)[0], "e4m3", 128, "window")
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+def test_a_layer_without_an_index(kv):
+    """Caches without compressed keys and ring give the bits of those with them."""
+    from sparse_attention_decode_compress_b200 import QSACache, qsa_compress_append
+    Hq, Hkv, D, lens = 16, 2, 128, [300, 200]
+    outs = []
+    for idx_dim, rows in ((32, 2), (0, 0)):
+        c = A.PagedKV(lens, Hkv, D, kv, 16, "cuda", seed=155)
+        full = c.cache()
+        cache = QSACache.allocate(full.k_cache, full.v_cache, full.block_table, idx_dim, rows,
+                                  k_scale=full.k_scale, v_scale=full.v_scale)
+        x = queries((2, Hq + 2 * Hkv, D), kv, 156).cuda()
+        q = QSARopeAppend(cache, Hq)(ints([n - 1 for n in lens]), ints([0, 1, 2]), x[:, :Hq], x[:, Hq:Hq + Hkv],
+                                     x[:, Hq + Hkv:])
+        outs.append([q, cache.k_cache, cache.v_cache,
+                     *QSAWindowDecode(cache, 2, 1, Hq, 100, 4)(q.unsqueeze(1), ints(lens)),
+                     *QSAWindowPrefill(cache, 2, 2, 1, Hq, 100, 4)(q, ints([0, 1, 2]), ints(lens)),
+                     *QSAPrefixDecode(cache, 2, 1, Hq, 2, 1, 64, 236)(q.unsqueeze(1), ints(lens), ints([0, 1, 2]),
+                                                                      ints([64, 64]))])
+    for a, b in zip(*outs):
+        assert torch.equal(a.float(), b.float())
+    with pytest.raises(RuntimeError):
+        qsa_compress_append(cache, ints([0, 0]), ints([0, 1, 2]), torch.zeros((2, 32), dtype=torch.int8, device="cuda"), 1)
