@@ -917,3 +917,42 @@ def test_a_layer_without_an_index(kv):
         assert torch.equal(a.float(), b.float())
     with pytest.raises(RuntimeError):
         qsa_compress_append(cache, ints([0, 0]), ints([0, 1, 2]), torch.zeros((2, 32), dtype=torch.int8, device="cuda"), 1)
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+def test_appended_rows_are_what_the_sparse_decode_reads(kv):
+    """Prompts and then single tokens, rotated and appended, attended by the
+    sparse decode over every block: dense attention of the same rows."""
+    from sparse_attention_decode_compress_b200 import (new_workspace, qsa_sparse_decode_merged,
+                                                       qsa_sparse_decode_workspace_bytes)
+    Hq, Hkv, D, page, B, S = 16, 2, 128, 16, 3, 2
+    lens = [70, 33, 101]
+    c = A.PagedKV([n + 4 for n in lens], Hkv, D, kv, page, "cuda", seed=161)
+    if kv == "e4m3":  # scales that the appended rows fit
+        c.k_scale.fill_(2.0 ** -5)
+        c.v_scale.fill_(2.0 ** -5)
+    c.k.zero_()
+    c.v.zero_()
+    cache = c.cache()
+    rope = QSARopeAppend(cache, Hq, theta=1e6)
+
+    def append(pos, new, seed):
+        x = queries((sum(new), Hq + 2 * Hkv, D), kv, seed).cuda()
+        cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+        return rope(ints(pos), ints(cu), x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:])
+
+    append([0] * B, lens, 162)
+    for step in range(3):
+        q = append([n + step for n in lens], [1] * B, 163 + step).view(B, 1, Hq, D)
+        now = [n + step + 1 for n in lens]
+        topk = max(-(-n // 4) for n in now)
+        sel = torch.full((B, topk), -1, dtype=torch.int32)
+        for r, n in enumerate(now):
+            sel[r, :-(-n // 4)] = torch.arange(-(-n // 4))
+        f32 = dict(dtype=torch.float32, device="cuda")
+        o_part, lse_part = torch.empty((S, B, 1, Hq, D), **f32), torch.empty((S, B, 1, Hq), **f32)
+        o, lse = torch.empty((B, 1, Hq, D), **f32), torch.empty((B, 1, Hq), **f32)
+        ws = new_workspace(qsa_sparse_decode_workspace_bytes(B, 1, Hq, Hkv, D, topk, S), "cuda")
+        qsa_sparse_decode_merged(cache, q, ints(now), sel.cuda(), D ** -0.5, S, o_part, lse_part, o, lse, ws)
+        c.k, c.v = cache.k_cache.cpu(), cache.v_cache.cpu()
+        A.check(o, lse, prefix_want(c, q.cpu(), now, 1), kv, D, f"step {step}")
