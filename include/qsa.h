@@ -467,12 +467,13 @@ qsa_status qsa_sparse_prefill(const qsa_cache *cache, int32_t B, int32_t n_token
  * (a padding row of a batch) is one.  Keys that no query of a call sees are
  * never read, and their pages may be unmapped (-1).  K and V rows that some
  * query of the call sees have to be finite where another query of the same
- * request does not see them.
+ * request (of its group, for a shared prefix) does not see them.
  * Lengths, offsets and tables live on the device; the host bounds (max_...)
  * size the launch.  Recorded on the device: QSA_ERR_BOUNDS for a length that
  * the block table cannot hold (cut to what it can) and for a missing page (its
- * keys and values read as zeros); QSA_ERR_BAD_INPUT for malformed offsets
- * (their rows are left out).
+ * keys and values read as zeros); by the attention calls QSA_ERR_BAD_INPUT for
+ * malformed offsets (their rows are left as they were; qsa_prefix_decode says
+ * what its requests get).
  * Workspaces: 256-byte aligned, any contents, nothing is kept between calls;
  * calls that overlap on the GPU (captured graphs too) need separate ones.  Where
  * a *_workspace_bytes call returns 0 the workspace may be NULL.

@@ -49,10 +49,15 @@ AttnPlan plan_stream(long long seqs, int Hkv, long long span, bool merge) {
   p.tiles = 1;
   const long long pairs = std::max(1LL, seqs * Hkv);
   if (merge) {
-    // two CTAs an SM (batch 32 x 32k, window 4,096: 39.6 us a single pass against
-    // 43.1 with four and 47.5 with eight), none with more than 16,384 keys; up to 8
-    // of a row form a cluster, also where there is room for more, up to 1,024 keys
-    // each
+    // two CTAs an SM: batch 32 x 32k, window 4,096 takes 21.1 us in a graph (partly
+    // from L2), 33.7 with one and 27.4 with four; 16 x 2,000 keys of 8 kv heads 20.4,
+    // 31.5 and 25.8; four query tokens, batch 64, 39.7, 60.4 and 49.6.  Up to 8 of a
+    // row form a cluster, also where there is room for more, up to 1,024 keys each.
+    // None takes more than 16,384 keys of the longest request that the block table
+    // can hold (lengths are on the device), so that one long request does not run on
+    // few SMs: dense, a table for 1M tokens, 127 requests of 4,000 and one of 1M
+    // take 0.46 ms, 11.1 without this bound.  Short requests pay for such a table:
+    // 128 of 2,000 take 227 us, 34 without the bound, 256 of 8,192 586 and 236.
     p.splits = (int)std::max(1LL, std::min({2LL * kPlanSMs / pairs, ceil_ll(span, 128), 64LL}));
     p.splits = (int)std::max<long long>(p.splits, std::min(ceil_ll(span, 16384), 64LL));
     if (p.splits > kMaxCluster && span <= 1024LL * kMaxCluster) p.splits = kMaxCluster;
@@ -307,7 +312,10 @@ qsa_status launch_rope(const qsa::rope::Params &p, bool vec, int layout, cudaStr
   const long long few = (long long)p.n_tok * ceil_ll(heads, kStep);
   // one step a warp while that leaves the GPU room (128 tokens: latency), NB steps,
   // all loaded at once, for more: 22,000 tokens of 40 heads take 99 us with one,
-  // 76, 74, 73 and 72 with two to five (four times the registers from there on)
+  // 76, 74, 73 and 72 with two to five (four times the registers from there on).
+  // The last warp of a token takes what is left: parts alike in its place were
+  // slower for every head count (16,000 tokens: 24 heads 36.9 against 36.0 us, 36
+  // 48.3 and 47.5, 44 59.9 and 59.0, 40 52.6 and 52.2).
   const bool one = few <= 16LL * kPlanSMs;
   const long long warps = (long long)p.n_tok * ceil_ll(heads, kStep * (one ? 1 : NB));
   const long long grid = ceil_ll(warps * 32, kThreads);

@@ -21,9 +21,12 @@
 //
 // Measured (B200): batch 32, 16 / 2 heads, window 4,096 + 64 keys, bf16: 27.4 us,
 // 5.0 TB/s (77 % of the measured copy rate; one wave of CTAs starts and ends in
-// that); four query tokens, batch 64, window 2,000: 39.8 us, 3.2 TB/s (32 rows a
-// kv head: Q fragments come from shared memory at every stage); fp8, batch 256,
-// 32 / 4 heads: 154 us, 4.5 TB/s (instruction issue: conversions and addresses).
+// that); four query tokens, batch 64, window 2,000: 39.5 us, 3.2 TB/s (32 rows a
+// kv head: Q fragments come from shared memory at every stage, and 255 registers
+// leave 1.7 warps a scheduler, which wait for the instruction before: it issues 34 %
+// of the time); fp8, batch 256, 32 / 4 heads: 154 us, 4.5 TB/s (the same wait
+// with 2.6 warps a scheduler: issue 54 %, ALU 52 %, and 2.3 waves of CTAs, the SMs
+// active for 83 % of the kernel).
 #pragma once
 #include "attn_common.cuh"
 #include "sparse_decode_warp.cuh"

@@ -39,10 +39,11 @@
 // largest one seen, on the weight before it is rounded to f16 (2^-11, and what
 // f8_ref says about small ones).
 //
-// Measured (B200): 8,192 tokens of 32 heads over a window of 8,192 in 0.97 ms
-// (1.13 PFLOP/s, 66 % of the measured cuBLAS burst rate; 1.1 ms repeated, under
-// the power limit); 4 x 1,024 tokens of 16 heads over 4,096 in 164 us (850
-// TFLOP/s, on 1.73 waves of CTAs).  A step of 256 rows x 128 keys takes about
+// Measured (B200): 8,192 tokens of 32 heads over a window of 8,192 in 1.10 ms, call
+// after call (1.0 PFLOP/s, 58 % of the measured cuBLAS burst rate and 69 % of its
+// sustained one: the power limit holds here too; a first call in 0.97); 4 x 1,024
+// tokens of 16 heads over 4,096 in 164 us (855 TFLOP/s, on 1.73 waves of CTAs); from
+// an fp8 cache 1.6 and 1.4 times as long (631 and 516 TFLOP/s).  A step of 256 rows x 128 keys takes about
 // 3,500 cycles, 2,048 of them products: scores, weights, values and next scores
 // follow one another, and with two tiles the tensor core waits for softmax.
 #pragma once

@@ -18,10 +18,11 @@
 // token (or a share of its heads): the two angles a lane computes are passed
 // around by shuffles, every lane keeps the 8 (cos, sin) pairs of its place in
 // the head and applies them to one head after another, 16 bytes at a time.
-// Measured (B200): 22,152 tokens of 32 / 4 heads, D 128, bf16: 72.8 us, 6.2 TB/s
-// (97 % of the measured copy rate); 4,096 tokens of 16 / 2 heads: 11.3 us (one
+// Measured (B200): 22,152 tokens of 32 / 4 heads, D 128, bf16: 74.7 us, 6.1 TB/s
+// (94 % of the measured copy rate); 4,096 tokens of 16 / 2 heads: 11.3 us (one
 // wave of warps, whose chain request -> position -> page -> store is exposed);
-// 128 tokens: 2.8 us in a graph.
+// 128 tokens: 2.8 us in a graph.  16,384 tokens of 32 / 4 heads, L2 flushed: bf16
+// 59.4 us, from bf16 into fp8 pages 71.7, float32 106.6 (floors 51.9, 49.4, 103.9).
 #pragma once
 #include "qsa_common.cuh"
 
