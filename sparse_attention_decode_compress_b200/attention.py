@@ -5,11 +5,12 @@ Each C entry point has a function of its name, which checks its arguments and
 marshals them, and a class that holds what a serving loop keeps between calls
 (the cache description, the output buffers and the workspace).  A class takes
 the cache's tensors when it is made and keeps them: their contents may change; a
-tensor put in the place of one later is not seen.  Its outputs are its own buffers, overwritten by its next
-call.  Work goes to `stream`, by default the current stream of the tensors'
-device; a handle may be made on one stream and called on others, one at a time,
-and dropped while its last call still runs (on a torch.cuda.ExternalStream only
-after that: torch cannot order memory behind such a stream's work safely).
+tensor put in the place of one later is not seen.  Its outputs are its own
+buffers, overwritten by its next call.  Work goes to `stream`, by default the
+current stream of the tensors' device; a handle may be made on one stream and
+called on others, one call at a time, and dropped while its last call still runs
+(on a torch.cuda.ExternalStream only after that: torch cannot order memory behind
+such a stream's work safely).
 """
 from __future__ import annotations
 

@@ -25,27 +25,28 @@
 // A step's weights are relative to the maximum of the steps BEFORE it: they
 // need not wait for their own (which runs beside them), and float32 and bf16
 // lose nothing by weights above 1.  When a row's maximum has grown by more than
-// 2^8 (f16 weights: 2^4) the next step starts with rescaling its sum and its output accumulators,
-// which stay in tensor memory; the scores of step j are issued behind the values
-// of step j - 1, so the thread that owns the row has them to itself then.  Only
-// growth beyond the weights' range (2^60; f16 weights: 2^4) makes 32 keys start
-// again with their own maximum.
+// 2^8 (f16 weights: 2^4) the next step starts with rescaling its sum and its
+// output accumulators, which stay in tensor memory; the scores of step j are
+// issued behind the values of step j - 1, so the thread that owns the row has them
+// to itself then.  Only growth beyond the weights' range (2^60; f16 weights: 2^4)
+// makes 32 keys start again with their own maximum.
 //
 // Rounding: weights to bf16, the error of the output's own rounding; where 32 keys
-// start again, the weights of the step's keys before them are rounded once more.  fp8
-// caches run in f16, which holds every E4M3 code: queries scaled per row by a
-// power of two (fp8_frag.cuh says what that keeps), the key scale on the score
-// in float32, and the value scale, relative to a power of two that follows the
+// start again, the weights of the step's keys before them are rounded once more.
+// fp8 caches run in f16, which holds every E4M3 code: queries scaled per row by a
+// power of two (fp8_frag.cuh says what that keeps), the key scale on the score in
+// float32, and the value scale, relative to a power of two that follows the
 // largest one seen, on the weight before it is rounded to f16 (2^-11, and what
 // f8_ref says about small ones).
 //
 // Measured (B200): 8,192 tokens of 32 heads over a window of 8,192 in 1.10 ms, call
 // after call (1.0 PFLOP/s, 58 % of the measured cuBLAS burst rate and 69 % of its
 // sustained one: the power limit holds here too; a first call in 0.97); 4 x 1,024
-// tokens of 16 heads over 4,096 in 164 us (855 TFLOP/s, on 1.73 waves of CTAs); from
-// an fp8 cache 1.6 and 1.4 times as long (631 and 516 TFLOP/s).  A step of 256 rows x 128 keys takes about
-// 3,500 cycles, 2,048 of them products: scores, weights, values and next scores
-// follow one another, and with two tiles the tensor core waits for softmax.
+// tokens of 16 heads over 4,096 in 163 us (855 TFLOP/s, on 1.73 waves of CTAs); from
+// an fp8 cache 1.6 and 1.4 times as long (631 and 516 TFLOP/s).  A step of 256 rows
+// x 128 keys takes about 3,500 cycles, 2,048 of them products: scores, weights,
+// values and next scores follow one another, and with two tiles the tensor core
+// waits for softmax.
 #pragma once
 #include "attn_common.cuh"
 #include "fp8_frag.cuh"
