@@ -32,7 +32,7 @@
 // makes 32 keys start again with their own maximum.
 //
 // Rounding: weights to bf16, the error of the output's own rounding; where 32 keys
-// start again, the weights of the step's keys before them are rounded once more.
+// start again, the weights of the step's keys before them follow by a power of two.
 // fp8 caches run in f16, which holds every E4M3 code: queries scaled per row by a
 // power of two (fp8_frag.cuh says what that keeps), the key scale on the score in
 // float32, and the value scale, relative to a power of two that follows the
@@ -391,9 +391,15 @@ __device__ __forceinline__ void weights(uint32_t s_at, uint32_t o_at, bool first
       // these keys' maximum; the weights in place follow
       pre::tmem_ld_wait();
       tmem_st_wait();
-      const float old = r.mx;
-      rebase<D, FP8>(r, top > r.mx ? top : r.mx, r.vref, first, o_at);
-      const float al = old == -INFINITY ? 0.f : ex2(old - r.mx);
+      // (rows that are out of range alone, the others' by a factor of one; a power
+      // of two where there are weights to follow, so that none is rounded again)
+      float to = r.mx, al = 1.f;
+      if (top > r.mx + kRange) {
+        const float k = floorf(top - r.mx);  // inf: the row's first keys
+        to = k < INFINITY ? r.mx + k : top;
+        al = k < 126.f ? __int_as_float((127 - (int)k) << 23) : 0.f;
+      }
+      rebase<D, FP8>(r, to, r.vref, first, o_at);
 #pragma unroll 1
       for (int k = 0; k < q; ++k) {
         uint32_t w[16];

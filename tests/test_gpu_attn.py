@@ -956,3 +956,35 @@ def test_appended_rows_are_what_the_sparse_decode_reads(kv):
         qsa_sparse_decode_merged(cache, q, ints(now), sel.cuda(), D ** -0.5, S, o_part, lse_part, o, lse, ws)
         c.k, c.v = cache.k_cache.cpu(), cache.v_cache.cpu()
         A.check(o, lse, prefix_want(c, q.cpu(), now, 1), kv, D, f"step {step}")
+
+
+# --------------------------------------------------- each weight once rounded --
+@pytest.mark.parametrize("kv", ["f32", "bf16", "e4m3"])
+def test_weights_are_rounded_once(kv):
+    """Rows of a chunk whose windows begin in the first and in the second 32 keys
+    of a tile.  The first ones' weights 2^-c, c = 1 - log2(1 + 2^-8 + 2^-11), round
+    up to bf16 by nearly 2^-8, and so would their products with another 2^-c, the
+    factor of a maximum that is higher by one step: rounded again behind the keys
+    that the second ones start with, they would be off by 2^-7.  The two keys of
+    the maxima have values of zero, the others 128 values that share the error."""
+    D, page, n, window, first = 128, 64, 32, 100, 16
+    L = first + n - 1 + window  # token i sees the keys from first + i on
+    c = A.PagedKV([L], 1, D, kv, page, "cuda", seed=171)
+    if kv == "e4m3":
+        c.k_scale.fill_(1.0)
+        c.v_scale.fill_(1.0)
+    typ = c.k.dtype
+    k, v = torch.zeros((L, D)), torch.zeros((L, D))
+    k[:, 0] = -8.0
+    k[first:31, 0], k[31, 0], k[40, 0] = -1.0, 0.0, 1.0
+    v[first:31] = 1 + torch.arange(D) / 128
+    for t in range(L):
+        pg = int(c.table_host[0, t // page])
+        c.k[pg, t % page, 0], c.v[pg, t % page, 0] = k[t].to(typ), v[t].to(typ)
+    q = torch.zeros((n, 1, D), dtype=torch.float32 if kv == "f32" else torch.bfloat16)
+    q[..., 0] = 1.0
+    scale = (1 - math.log2(1 + 2.0 ** -8 + 2.0 ** -11)) * math.log(2)
+    keys = [A.visible(L - n + i, window, 0) for i in range(n)]
+    want = A.stack([A.attend(q[i], c.values("k", 0, keys[i]), c.values("v", 0, keys[i]), scale) for i in range(n)])
+    o, lse = QSAWindowPrefill(c.cache(), 1, n, n, 1, window, sm_scale=scale)(q.cuda(), ints([0, n]), ints([L]))
+    A.check(o, lse, want, kv, D, "chunk")
