@@ -459,8 +459,8 @@ qsa_status qsa_sparse_prefill(const qsa_cache *cache, int32_t B, int32_t n_token
  *   - FP8 values are code * scale[page][kv head];
  *   - sums, softmax statistics and partial results are float32; for BF16 and
  *     FP8 caches the softmax weights enter the value product rounded to 16
- *     bits: relative 2^-9 (bf16), less than the error of o's own rounding; for
- *     FP8 caches, whose weights carry the V scale, relative 2^-11 down to 2^-24
+ *     bits, once: relative 2^-8 (bf16), the error of o's own rounding; for FP8
+ *     caches, whose weights carry the V scale, relative 2^-11 down to 2^-24
  *     of the largest (weight times scale) of the row, 2^-8 down to 2^-27, and
  *     an error of 2^-35 of that largest one at most for those below.
  * A query that sees no key gives o = 0 and lse = -inf; a request of length 0

@@ -15,7 +15,7 @@
 // through the workspace.  fp8 tiles go from shared memory into f16 fragments
 // (fp8_frag.cuh).
 //
-// Weights p = exp(s - max) enter the value product rounded to bf16 (2^-9
+// Weights p = exp(s - max) enter the value product rounded to bf16 (2^-8
 // relative; o is rounded to bf16 itself) or, times the V scale, to f16 (2^-11, and
 // what f8_ref says about small ones).
 //
