@@ -615,7 +615,7 @@ qsa_status qsa_window_prefill(const qsa_cache *cache, int32_t B, int32_t n_token
  * and the tail are two partial results merged by log-sum-exp, as the KV
  * partitions of qsa_sparse_decode are.
  *
- *   cu_group [n_groups+1], prefix_lens [n_groups] int32; a request in no
+ *   cu_group [n_groups+1], prefix_lens [n_groups] int32, n_groups 1 .. B; a request in no
  *            group (before cu_group[0], from cu_group[n_groups] on) shares
  *            nothing; a group may be empty, a prefix 0
  *   max_group   host bound of a group's requests, 1 .. B; a larger group is
